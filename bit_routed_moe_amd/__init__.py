@@ -17,6 +17,8 @@ __all__ = [
     "forward_noalloc", "forward_noalloc_max_bytes",
     "workspace_bytes", "workspace_region", "WS_REGION", "dequantize", "quantize_mxfp8", "status_string", "version",
     "EXPORTS", "STAGE", "set_stage_events",
+    "ACT", "Matmul", "make_matmul", "matmul_workspace_bytes", "linear", "linear_backward", "grouped_matmul",
+    "grouped_matmul_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libds4moe.so")
@@ -24,6 +26,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libds4moe.s
 WFMT = {"q2k": 1, "mxfp4": 2, "bf16": 3, "q4k": 4}
 DTYPE = {"f32": 0, "bf16": 1, "fp8": 2}
 ALGO = {"auto": 0, "gemv": 1, "grouped": 2}
+ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5}
 
 # Every entry point declared in include/ds4moe.h.
 EXPORTS = (
@@ -31,6 +34,8 @@ EXPORTS = (
     "ds4moe_workspace_bytes", "ds4moe_dequantize", "ds4moe_status_string", "ds4moe_last_error",
     "ds4moe_version", "ds4moe_set_stage_events", "ds4moe_forward_path", "ds4moe_quantize_mxfp8",
     "ds4moe_workspace_region", "ds4moe_forward_noalloc", "ds4moe_forward_noalloc_max_bytes",
+    "ds4moe_linear", "ds4moe_linear_backward", "ds4moe_grouped_matmul", "ds4moe_grouped_matmul_backward",
+    "ds4moe_matmul_workspace_bytes",
 )
 
 WS_REGION = {"topk_idx": 0, "topk_w": 1, "offsets": 2, "sorted_pair": 3, "pair_pos": 4, "active": 5,
@@ -47,6 +52,11 @@ class Config(ctypes.Structure):
 class Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "gate", "up", "down", "gate_scales", "up_scales", "down_scales", "sh_gate", "sh_up", "sh_down")]
+
+
+class Matmul(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("in_dim", "out_dim", "groups", "dtype", "act", "grad_dtype")] +
+                [(n, ctypes.c_int64) for n in ("ldx", "ldw", "ldy", "ldz")])
 
 
 class Ds4MoeError(RuntimeError):
@@ -66,6 +76,7 @@ def _load():
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     cfgp, wp = ctypes.POINTER(Config), ctypes.POINTER(Weights)
+    mmp = ctypes.POINTER(Matmul)
     sigs = {
         "ds4moe_router_logits": (i32, [cfgp, i32, vp, vp, vp, vp]),
         "ds4moe_route": (i32, [cfgp, i32, vp, vp, vp, vp]),
@@ -84,6 +95,11 @@ def _load():
         "ds4moe_workspace_region": (i32, [cfgp, i32, i32, ctypes.POINTER(sz), ctypes.POINTER(sz)]),
         "ds4moe_forward_noalloc": (i32, [cfgp, wp, i32, vp, vp, vp, vp]),
         "ds4moe_forward_noalloc_max_bytes": (sz, []),
+        "ds4moe_linear": (i32, [mmp, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "ds4moe_linear_backward": (i32, [mmp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "ds4moe_grouped_matmul": (i32, [mmp, i32, vp, i32, vp, vp, vp, vp, i32, vp, vp, vp, sz, vp]),
+        "ds4moe_grouped_matmul_backward": (i32, [mmp, i32, vp, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]),
+        "ds4moe_matmul_workspace_bytes": (sz, [mmp, i32, i32]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -215,3 +231,67 @@ def set_stage_events(stage, start=None, stop=None):
     on this thread; "router_proj" times ds4moe_router_logits; no events clears."""
     h = lambda e: None if e is None else ctypes.c_void_p(e.cuda_event)
     _check(lib.ds4moe_set_stage_events(STAGE[stage] if isinstance(stage, str) else stage, h(start), h(stop)))
+
+
+# ---- products at original precision -------------------------------------------
+
+def make_matmul(in_dim, out_dim, groups=1, dtype="bf16", act="none", grad=None, ldx=0, ldw=0, ldy=0,
+                ldz=0) -> Matmul:
+    """Descriptor of a dense or grouped product: weights [groups][out_dim][in_dim],
+    `act` a key of ACT, `grad` the type of dw and dbias (default: dtype), row
+    strides in elements (0: no gaps)."""
+    return Matmul(in_dim, out_dim, groups, DTYPE[dtype], ACT[act], DTYPE[grad or dtype], ldx, ldw, ldy, ldz)
+
+
+def matmul_workspace_bytes(m: Matmul, rows: int, backward: bool = False) -> int:
+    return int(lib.ds4moe_matmul_workspace_bytes(ctypes.byref(m), rows, int(backward)))
+
+
+def _d(*tensors):
+    """Device pointers of tensors (or None), all on the current HIP device."""
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise Ds4MoeError(-1, f"tensor on {t.device}, not on the current HIP device {dev}")
+    return [None if t is None else t.data_ptr() for t in tensors]
+
+
+def _ws(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def linear(m, rows, x, w, y, bias=None, residual=None, z=None, workspace=None, stream=None):
+    """y = act(x W^T + bias) + residual; z (optional) receives the pre-activations."""
+    px, pw, pb, pr, py, pz, ps = _d(x, w, bias, residual, y, z, workspace)
+    _check(lib.ds4moe_linear(ctypes.byref(m), rows, px, pw, pb, pr, py, pz, ps, _ws(workspace), _s(stream)))
+
+
+def linear_backward(m, rows, x, w, dy, z=None, dx=None, dw=None, dbias=None, workspace=None, stream=None):
+    """Gradients of linear: each of dx, dw, dbias that is given."""
+    px, pw, pz, pdy, pdx, pdw, pdb, ps = _d(x, w, z, dy, dx, dw, dbias, workspace)
+    _check(lib.ds4moe_linear_backward(ctypes.byref(m), rows, px, pw, pz, pdy, pdx, pdw, pdb, ps, _ws(workspace),
+                                      _s(stream)))
+
+
+def grouped_matmul(m, rows, x, w, expert_offsets, y, sorted_pair=None, top_k=1, x_rows=None, bias=None, z=None,
+                   workspace=None, stream=None):
+    """Products of expert-sorted rows with their experts' weights, from
+    permute's expert_offsets (and sorted_pair, when rows are read from the
+    tokens' x)."""
+    px, pw, pb, po, pp, py, pz, ps = _d(x, w, bias, expert_offsets, sorted_pair, y, z, workspace)
+    xr = x.shape[0] if x_rows is None else x_rows
+    _check(lib.ds4moe_grouped_matmul(ctypes.byref(m), rows, px, xr, pw, pb, po, pp, top_k, py, pz, ps,
+                                     _ws(workspace), _s(stream)))
+
+
+def grouped_matmul_backward(m, rows, x, w, expert_offsets, dy, z=None, sorted_pair=None, top_k=1, x_rows=None,
+                            dx=None, dw=None, dbias=None, workspace=None, stream=None):
+    """Gradients of grouped_matmul: each of dx (a row per sorted row), dw,
+    dbias that is given.  x is read for dw only, but its row count is always
+    part of the call (x_rows, if x is None)."""
+    px, pw, pz, pdy, po, pp, pdx, pdw, pdb, ps = _d(x, w, z, dy, expert_offsets, sorted_pair, dx, dw, dbias,
+                                                    workspace)
+    xr = x_rows if x_rows is not None else (x.shape[0] if x is not None else rows)
+    _check(lib.ds4moe_grouped_matmul_backward(ctypes.byref(m), rows, px, xr, pw, pz, pdy, po, pp, top_k, pdx, pdw,
+                                              pdb, ps, _ws(workspace), _s(stream)))

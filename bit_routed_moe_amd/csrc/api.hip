@@ -9,6 +9,7 @@
 
 #include "ds4moe.h"
 #include "launch.hpp"
+#include "matmul.hpp"
 
 namespace ds4 {
 thread_local StageEvents g_stage_events[N_STAGES] = {};
@@ -302,6 +303,193 @@ bool batch1_path(const ds4moe_config* cfg, int32_t T) {
            ds4::t1_supported(cfg->wfmt, cfg->hidden, cfg->ffn, cfg->shared_ffn, cfg->n_experts, cfg->top_k);
 }
 
+// ---- products at original precision ---------------------------------------------
+
+// Largest product of two of a call's sizes: grids and element counts stay
+// below 2^32 workgroups' threads at the smallest tiles (64 x 64).
+constexpr int64_t MM_MAX_ELEMS = (int64_t)1 << 36;
+
+int check_ld(const char* name, int64_t ld, int64_t cols, int64_t q) {
+    if (ld < cols) return fail(DS4MOE_E_SHAPE, "%s %lld is below the row's %lld elements", name, (long long)ld,
+                               (long long)cols);
+    if (ld % q) return fail(DS4MOE_E_SHAPE, "%s %lld is not a whole number of 16 bytes", name, (long long)ld);
+    if (ld > ((int64_t)1 << 31)) return fail(DS4MOE_E_SHAPE, "%s %lld", name, (long long)ld);
+    return DS4MOE_OK;
+}
+
+// Validates a descriptor (strides aside, which depend on the tensors present).
+int check_mm(const ds4moe_matmul* m, int32_t rows) {
+    if (!m) return fail(DS4MOE_E_ARG, "m is NULL");
+    if (m->dtype != DS4MOE_DT_F32 && m->dtype != DS4MOE_DT_BF16) {
+        if (m->dtype == DS4MOE_DT_FP8_E4M3) return fail(DS4MOE_E_UNSUPPORTED, "fp8 products");
+        return fail(DS4MOE_E_ARG, "dtype %d", m->dtype);
+    }
+    if (m->grad_dtype != DS4MOE_DT_F32 && m->grad_dtype != DS4MOE_DT_BF16) {
+        if (m->grad_dtype == DS4MOE_DT_FP8_E4M3) return fail(DS4MOE_E_UNSUPPORTED, "fp8 gradients");
+        return fail(DS4MOE_E_ARG, "grad_dtype %d", m->grad_dtype);
+    }
+    if (m->dtype == DS4MOE_DT_F32 && m->grad_dtype != DS4MOE_DT_F32)
+        return fail(DS4MOE_E_UNSUPPORTED, "fp32 products have fp32 gradients");
+    if (m->act < DS4MOE_ACT_NONE || m->act > DS4MOE_ACT_SWIGLU) return fail(DS4MOE_E_ARG, "act %d", m->act);
+    if (m->in_dim < 1 || m->in_dim > (1 << 20)) return fail(DS4MOE_E_SHAPE, "in_dim %d not in [1, 2^20]", m->in_dim);
+    if (m->out_dim < 1 || m->out_dim > (1 << 20))
+        return fail(DS4MOE_E_SHAPE, "out_dim %d not in [1, 2^20]", m->out_dim);
+    if (m->act == DS4MOE_ACT_SWIGLU && m->out_dim % 2)
+        return fail(DS4MOE_E_SHAPE, "SwiGLU needs an even out_dim, not %d", m->out_dim);
+    if (m->groups < 1 || m->groups > 1024) return fail(DS4MOE_E_SHAPE, "groups %d not in [1, 1024]", m->groups);
+    if (rows < 1 || rows > (1 << 24)) return fail(DS4MOE_E_SHAPE, "rows %d not in [1, 2^24]", rows);
+    if ((int64_t)rows * m->in_dim > MM_MAX_ELEMS || (int64_t)rows * m->out_dim > MM_MAX_ELEMS ||
+        (int64_t)m->in_dim * m->out_dim > MM_MAX_ELEMS)
+        return fail(DS4MOE_E_SHAPE, "%d rows of %d x %d: a product of two sizes is above 2^36", rows, m->out_dim,
+                    m->in_dim);
+    return DS4MOE_OK;
+}
+
+int64_t mm_quantum(const ds4moe_matmul* m) { return m->dtype == DS4MOE_DT_F32 ? 4 : 8; }
+
+// Row splits of the bias gradient: about 64 rows each when the groups are
+// even, at most 64 splits.
+int mm_splits(const ds4moe_matmul* m, int32_t rows) {
+    const int64_t s = ((int64_t)rows + 64 * (int64_t)m->groups - 1) / (64 * (int64_t)m->groups);
+    return (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
+}
+
+int mm_max_chunks(const ds4moe_matmul* m, int32_t rows, int bm) {
+    return rows / bm + (m->groups < rows ? m->groups : rows);
+}
+
+struct MmLayout {
+    size_t plan, dz, partial, total;
+};
+
+// Workspace of a call (sizes grow with rows: the plan is sized for the
+// smallest chunks).
+MmLayout mm_layout(const ds4moe_matmul* m, int32_t rows, bool backward) {
+    MmLayout L{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = align256(off);
+        off = o + bytes;
+        return o;
+    };
+    const bool f32 = m->dtype == DS4MOE_DT_F32;
+    L.plan = take(m->groups > 1 ? 256 + sizeof(ds4::MmChunk) * (size_t)mm_max_chunks(m, rows, ds4::MM_MIN_CHUNK) : 0);
+    if (backward) {
+        const int64_t q = mm_quantum(m);
+        const size_t lddz = (size_t)((m->out_dim + q - 1) / q * q);
+        L.dz = take(m->act != DS4MOE_ACT_NONE ? (size_t)rows * lddz * (f32 ? 4 : 2) : 0);
+        L.partial = take((size_t)mm_splits(m, rows) * m->groups * m->out_dim * 4);
+    }
+    L.total = align256(off);
+    return L;
+}
+
+// Fills the kernels' arguments; checks the strides of the tensors present.
+int mm_args(const ds4moe_matmul* m, int32_t rows, ds4::MmArgs& a, bool has_x, bool has_w, bool has_z) {
+    const int64_t q = mm_quantum(m);
+    const int64_t oc = m->act == DS4MOE_ACT_SWIGLU ? m->out_dim / 2 : m->out_dim;
+    a.P = rows;
+    a.K = m->in_dim;
+    a.N = m->out_dim;
+    a.E = m->groups;
+    a.act = m->act;
+    a.ldx = m->ldx ? m->ldx : m->in_dim;
+    a.ldw = m->ldw ? m->ldw : m->in_dim;
+    a.ldy = m->ldy ? m->ldy : oc;
+    a.ldz = m->ldz ? m->ldz : m->out_dim;
+    if (has_x) TRY(check_ld("ldx", a.ldx, m->in_dim, q));
+    if (has_w) TRY(check_ld("ldw", a.ldw, m->in_dim, q));
+    TRY(check_ld("ldy", a.ldy, oc, q));
+    if (has_z) TRY(check_ld("ldz", a.ldz, m->out_dim, q));
+    a.grad_f32 = m->grad_dtype == DS4MOE_DT_F32;
+    return DS4MOE_OK;
+}
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+    if (need == 0) return DS4MOE_OK;
+    if (!ws) return fail(DS4MOE_E_WORKSPACE, "workspace is NULL");
+    if (!aligned16(ws)) return fail(DS4MOE_E_ALIGN, "workspace not 16-byte aligned");
+    if (have < need) return fail(DS4MOE_E_WORKSPACE, "workspace %zu bytes < %zu needed", have, need);
+    return DS4MOE_OK;
+}
+
+int check_groups(const ds4moe_matmul* m, int32_t rows, int32_t x_rows, const int32_t* sorted_pair, int32_t top_k) {
+    if (sorted_pair) {
+        if (x_rows < 1 || x_rows > (1 << 24)) return fail(DS4MOE_E_SHAPE, "x_rows %d not in [1, 2^24]", x_rows);
+        if (top_k < 1) return fail(DS4MOE_E_SHAPE, "top_k %d", top_k);
+    } else if (x_rows != rows) {
+        return fail(DS4MOE_E_SHAPE, "x_rows %d must be rows (%d) without sorted_pair", x_rows, rows);
+    }
+    return DS4MOE_OK;
+}
+
+// The plan of a grouped call's chunks (none for one group of all rows).
+int mm_plan(const ds4moe_matmul* m, ds4::MmArgs& a, int mode, void* ws, const MmLayout& L, hipStream_t s) {
+    a.chunks = nullptr;
+    a.n_chunks = nullptr;
+    if (m->groups == 1) return DS4MOE_OK;
+    const int bm = ds4::mm_chunk_rows(m->dtype == DS4MOE_DT_F32, mode, a.P, a.K, a.N, a.E);
+    int32_t* n = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + L.plan);
+    ds4::MmChunk* c = reinterpret_cast<ds4::MmChunk*>(static_cast<uint8_t*>(ws) + L.plan + 256);
+    a.max_chunks = mm_max_chunks(m, a.P, bm);
+    TRY(hip_status(ds4::launch_mm_plan(a, bm, c, n, s), "matmul plan"));
+    a.chunks = c;
+    a.n_chunks = n;
+    return DS4MOE_OK;
+}
+
+int mm_backward_args(const ds4moe_matmul* m, int32_t rows, ds4::MmArgs& a, const void* x, const void* w,
+                     const void* z, const void* dy, void* dx, void* dw, void* dbias) {
+    TRY(mm_args(m, rows, a, dx || dw, dx || dw, m->act != DS4MOE_ACT_NONE));
+    if (!dx && !dw && !dbias) return fail(DS4MOE_E_ARG, "dx, dw and dbias are all NULL");
+    if (dw) REQ_PTR(x);
+    if (dx) REQ_PTR(w);
+    if (m->act != DS4MOE_ACT_NONE) REQ_PTR(z);
+    REQ_PTR(dy);
+    OPT_PTR(dx);
+    OPT_PTR(dw);
+    OPT_PTR(dbias);
+    a.x = x;
+    a.w = w;
+    a.zin = z;
+    a.dy = dy;
+    a.dx = dx;
+    a.dw = dw;
+    a.dbias = dbias;
+    return DS4MOE_OK;
+}
+
+int mm_forward(const ds4moe_matmul* m, ds4::MmArgs& a, void* ws, size_t bytes, hipStream_t s) {
+    const MmLayout L = mm_layout(m, a.P, false);
+    TRY(check_workspace(ws, bytes, L.total));
+    TRY(mm_plan(m, a, ds4::MM_FWD, ws, L, s));
+    return hip_status(ds4::launch_mm_forward(a, m->dtype == DS4MOE_DT_F32, s), "matmul");
+}
+
+int mm_backward(const ds4moe_matmul* m, ds4::MmArgs& a, void* ws, size_t bytes, hipStream_t s) {
+    const bool f32 = m->dtype == DS4MOE_DT_F32;
+    const MmLayout L = mm_layout(m, a.P, true);
+    TRY(check_workspace(ws, bytes, L.total));
+    a.splits = mm_splits(m, a.P);
+    a.partial = a.dbias ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.partial) : nullptr;
+    a.dz = a.dy;
+    a.lddz = a.ldy;
+    void* dz = nullptr;
+    if (a.act != DS4MOE_ACT_NONE && (a.dx || a.dw)) {
+        const int64_t q = mm_quantum(m);
+        dz = static_cast<uint8_t*>(ws) + L.dz;
+        a.dz = dz;
+        a.lddz = (a.N + q - 1) / q * q;
+    }
+    if (dz || a.dbias) TRY(hip_status(ds4::launch_mm_dz(a, f32, dz, s), "matmul backward: dz"));
+    if (a.dx) {
+        TRY(mm_plan(m, a, ds4::MM_DGRAD, ws, L, s));
+        TRY(hip_status(ds4::launch_mm_dgrad(a, f32, s), "matmul backward: dx"));
+    }
+    if (a.dw) TRY(hip_status(ds4::launch_mm_wgrad(a, f32, s), "matmul backward: dw"));
+    return ok();
+}
+
 }  // namespace
 
 extern "C" {
@@ -566,6 +754,89 @@ int ds4moe_dequantize(int32_t wfmt, const void* data, const void* scales, int64_
                                              static_cast<const uint8_t*>(scales), n, out_f32, out_bf16,
                                              static_cast<hipStream_t>(stream)),
                       "dequantize");
+}
+
+size_t ds4moe_matmul_workspace_bytes(const ds4moe_matmul* m, int32_t rows, int32_t backward) {
+    if (check_mm(m, rows) != DS4MOE_OK) return 0;
+    return mm_layout(m, rows, backward != 0).total;
+}
+
+int ds4moe_linear(const ds4moe_matmul* m, int32_t rows, const void* x, const void* w, const void* bias,
+                  const void* residual, void* y, void* z, void* workspace, size_t workspace_bytes, void* stream) {
+    TRY(check_mm(m, rows));
+    if (m->groups != 1) return fail(DS4MOE_E_SHAPE, "linear has one group, not %d", m->groups);
+    ds4::MmArgs a{};
+    TRY(mm_args(m, rows, a, true, true, z != nullptr));
+    REQ_PTR(x);
+    REQ_PTR(w);
+    OPT_PTR(bias);
+    OPT_PTR(residual);
+    REQ_PTR(y);
+    OPT_PTR(z);
+    a.x = x;
+    a.w = w;
+    a.bias = bias;
+    a.residual = residual;
+    a.y = y;
+    a.z = z;
+    a.x_rows = rows;
+    a.top_k = 1;
+    return mm_forward(m, a, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+int ds4moe_grouped_matmul(const ds4moe_matmul* m, int32_t rows, const void* x, int32_t x_rows, const void* w,
+                          const void* bias, const int32_t* expert_offsets, const int32_t* sorted_pair,
+                          int32_t top_k, void* y, void* z, void* workspace, size_t workspace_bytes, void* stream) {
+    TRY(check_mm(m, rows));
+    TRY(check_groups(m, rows, x_rows, sorted_pair, top_k));
+    ds4::MmArgs a{};
+    TRY(mm_args(m, rows, a, true, true, z != nullptr));
+    REQ_PTR(x);
+    REQ_PTR(w);
+    OPT_PTR(bias);
+    REQ_PTR(expert_offsets);
+    OPT_PTR(sorted_pair);
+    REQ_PTR(y);
+    OPT_PTR(z);
+    a.x = x;
+    a.w = w;
+    a.bias = bias;
+    a.offsets = expert_offsets;
+    a.sorted_pair = sorted_pair;
+    a.y = y;
+    a.z = z;
+    a.x_rows = x_rows;
+    a.top_k = sorted_pair ? top_k : 1;
+    return mm_forward(m, a, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+int ds4moe_linear_backward(const ds4moe_matmul* m, int32_t rows, const void* x, const void* w, const void* z,
+                           const void* dy, void* dx, void* dw, void* dbias, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    TRY(check_mm(m, rows));
+    if (m->groups != 1) return fail(DS4MOE_E_SHAPE, "linear has one group, not %d", m->groups);
+    ds4::MmArgs a{};
+    TRY(mm_backward_args(m, rows, a, x, w, z, dy, dx, dw, dbias));
+    a.x_rows = rows;
+    a.top_k = 1;
+    return mm_backward(m, a, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+int ds4moe_grouped_matmul_backward(const ds4moe_matmul* m, int32_t rows, const void* x, int32_t x_rows, const void* w,
+                                   const void* z, const void* dy, const int32_t* expert_offsets,
+                                   const int32_t* sorted_pair, int32_t top_k, void* dx, void* dw, void* dbias,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+    TRY(check_mm(m, rows));
+    TRY(check_groups(m, rows, x_rows, sorted_pair, top_k));
+    ds4::MmArgs a{};
+    TRY(mm_backward_args(m, rows, a, x, w, z, dy, dx, dw, dbias));
+    REQ_PTR(expert_offsets);
+    OPT_PTR(sorted_pair);
+    a.offsets = expert_offsets;
+    a.sorted_pair = sorted_pair;
+    a.x_rows = x_rows;
+    a.top_k = sorted_pair ? top_k : 1;
+    return mm_backward(m, a, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

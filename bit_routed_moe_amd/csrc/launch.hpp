@@ -9,6 +9,8 @@
 
 namespace ds4 {
 
+struct MmChunk;   // matmul.hpp
+
 enum Stage { STAGE_ROUTE = 0, STAGE_PERMUTE = 1, STAGE_FFN_UP = 2, STAGE_FFN_DOWN = 3, STAGE_COMBINE = 4,
              STAGE_ROUTER_PROJ = 5, N_STAGES = 6 };
 
@@ -128,5 +130,46 @@ hipError_t launch_layer_t1(const T1Params& p, hipStream_t s);
 
 hipError_t launch_combine(int act_bf16, int T, int H, int k, const void* expert_out, const int32_t* pair_pos,
                           const float* topk_w, const void* shared_out, void* y, hipStream_t s);
+
+// Products at original precision (matmul.hpp has the formulas).  Strides in
+// elements; rows start at 16-byte boundaries.
+struct MmArgs {
+    int P, K, N, E;             // rows, in_dim, out_dim (columns of z), groups
+    int act;
+    const void* x;              // [x_rows][ldx]
+    const void* w;              // [E][N][ldw]
+    const void* bias;           // [E][N] or null
+    const void* residual;       // [P][ldy] or null
+    void* y;                    // [P][ldy]
+    void* z;                    // [P][ldz] pre-activations, or null
+    int64_t ldx, ldw, ldy, ldz;
+    const int32_t* offsets;     // [E+1], null: one group of all rows
+    const int32_t* sorted_pair; // [P] pair ids, null: rows in order
+    int top_k, x_rows;
+    const MmChunk* chunks;      // row pieces of the groups, null: one group
+    const int32_t* n_chunks;
+    int max_chunks;             // chunks the grid covers
+    // backward
+    const void* dy;             // [P][ldy]
+    const void* zin;            // [P][ldz] pre-activations (act != none)
+    const void* dz;             // [P][lddz]
+    int64_t lddz;
+    void* dx;                   // [P][ldx]
+    void* dw;                   // [E][N][ldw]
+    void* dbias;                // [E][N]
+    bool grad_f32;              // dw and dbias in fp32 (else the rows' type)
+    int splits;                 // row splits of the bias gradient
+    float* partial;             // [splits][E][N]
+};
+
+// Rows per chunk of the plan that the forward or dgrad launch of these sizes uses.
+int mm_chunk_rows(bool f32, int mode, int P, int K, int N, int E);
+// One workgroup lists the chunks of the groups.
+hipError_t launch_mm_plan(const MmArgs& a, int chunk_rows, MmChunk* chunks, int32_t* n_chunks, hipStream_t s);
+hipError_t launch_mm_forward(const MmArgs& a, bool f32, hipStream_t s);
+hipError_t launch_mm_dgrad(const MmArgs& a, bool f32, hipStream_t s);
+hipError_t launch_mm_wgrad(const MmArgs& a, bool f32, hipStream_t s);
+// dz = dy * act'(z) into a.dz (act != none) and, with dbias, its column sums.
+hipError_t launch_mm_dz(const MmArgs& a, bool f32, void* dz, hipStream_t s);
 
 }  // namespace ds4

@@ -1,0 +1,192 @@
+// The plan of the grouped products, and the element-wise part of their
+// backward pass: dz = dy * act'(z) and the bias gradient (column sums of dz
+// over a group's rows).
+//
+// Memory-bound: dy and z are read once, dz is written once.  A workgroup takes
+// 256 columns (SwiGLU: 256 gate columns and the up columns they pair with) of
+// one split of a group's rows, 8 rows at a time, 8 columns per lane; the
+// column sums of unrounded dz stay in fp32 registers, are joined over the 8
+// row lanes in LDS and written as one partial per split, and a second launch
+// adds the partials in split order (no atomics: reproducible).
+#include "matmul.hpp"
+
+namespace ds4 {
+
+namespace {
+
+__global__ __launch_bounds__(1024) void mm_plan_kernel(const int32_t* __restrict__ offsets, int E, int P, int bm,
+                                                       MmChunk* __restrict__ chunks, int32_t* __restrict__ n_chunks,
+                                                       int cmax) {
+    __shared__ int tmp[32];
+    const int e = threadIdx.x;
+    int row0 = 0, n = 0;
+    if (e < E) mm_group_rows(offsets, e, P, row0, n);
+    const int nch = (n + bm - 1) / bm;
+    int total;
+    const int base = block_exclusive_scan(nch, tmp, &total);
+    for (int i = 0; i < nch && base + i < cmax; ++i) {   // (overlapping ranges of corrupt offsets stop at cmax)
+        MmChunk c;
+        c.group = e;
+        c.row0 = row0 + i * bm;
+        c.n = min(bm, n - i * bm);
+        c.pad = 0;
+        chunks[base + i] = c;
+    }
+    if (e == 0) n_chunks[0] = min(total, cmax);
+}
+
+constexpr int DZ_COLS = 256, DZ_ROWS = 8;
+
+// 8 elements of a row; vec: the address is 16-byte aligned and all 8 exist.
+template <typename T>
+__device__ __forceinline__ void dz_ld8(const T* p, int n, bool vec, float (&v)[8]) {
+    if (vec) {
+        if constexpr (sizeof(T) == 4) {
+            const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = a[i];
+                v[4 + i] = b[i];
+            }
+        } else {
+            const u32x4 a = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(a[i] << 16);
+                v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? mm_ld(p + i) : 0.0f;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void dz_st8(T* p, int n, bool vec, const float (&v)[8]) {
+    if (vec) {
+        if constexpr (sizeof(T) == 4) {
+            reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
+            reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+        } else {
+            u32x4 a;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            *reinterpret_cast<u32x4*>(p) = a;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) mm_st(p + i, v[i]);
+    }
+}
+
+template <typename T, bool GLU>
+__global__ __launch_bounds__(256) void mm_dz_kernel(MmArgs a, T* __restrict__ dz) {
+    constexpr int NP = GLU ? 2 : 1;
+    __shared__ float red[DZ_ROWS][NP * DZ_COLS + 4];
+    const int lc = threadIdx.x & 31, lr = threadIdx.x >> 5;
+    const int cols = GLU ? a.N >> 1 : a.N;
+    const int c = blockIdx.x * DZ_COLS + 8 * lc;
+    const int nc = min(8, cols - c);               // this lane's columns (<= 0: none)
+    int row0, n;
+    mm_group_rows(a.offsets, blockIdx.z, a.P, row0, n);
+    const int len = (n + a.splits - 1) / a.splits;
+    const int b = min(n, (int)blockIdx.y * len), e = min(n, b + len);
+    const bool vec = nc == 8, vecu = vec && (a.N & 15) == 0;   // (up columns start at N/2)
+    const T* dy = static_cast<const T*>(a.dy);
+    const T* zp = static_cast<const T*>(a.zin);
+    float sum[NP][8] = {};
+    if (nc > 0) {
+        for (int i = b + lr; i < e; i += DZ_ROWS) {
+            const size_t r = (size_t)(row0 + i);
+            float g[8], d[NP][8];
+            dz_ld8(dy + r * a.ldy + c, nc, vec, g);
+            if constexpr (GLU) {
+                float za[8], zb[8];
+                dz_ld8(zp + r * a.ldz + c, nc, vec, za);
+                dz_ld8(zp + r * a.ldz + cols + c, nc, vecu, zb);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float p = mm_sigmoid(za[j]);
+                    d[0][j] = g[j] * zb[j] * (p * (1.0f + za[j] * (1.0f - p)));
+                    d[1][j] = g[j] * (za[j] * p);
+                }
+            } else if (a.act != MM_NONE) {
+                float za[8];
+                dz_ld8(zp + r * a.ldz + c, nc, vec, za);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[0][j] = g[j] * mm_act_grad(za[j], a.act);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[0][j] = g[j];
+            }
+            if (dz) {
+                dz_st8(dz + r * a.lddz + c, nc, vec, d[0]);
+                if constexpr (GLU) dz_st8(dz + r * a.lddz + cols + c, nc, vecu, d[1]);
+            }
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[p][j] += d[p][j];
+        }
+    }
+    if (!a.partial) return;
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) red[lr][p * DZ_COLS + 8 * lc + j] = sum[p][j];
+    __syncthreads();
+    float* out = a.partial + ((size_t)blockIdx.y * a.E + blockIdx.z) * a.N;
+    for (int t = threadIdx.x; t < NP * DZ_COLS; t += 256) {
+        const int col = blockIdx.x * DZ_COLS + (t & (DZ_COLS - 1));
+        if (col >= cols) continue;
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < DZ_ROWS; ++i) s += red[i][t];
+        out[(t >= DZ_COLS ? cols : 0) + col] = s;
+    }
+}
+
+template <typename G>
+__global__ __launch_bounds__(256) void mm_dbias_kernel(const float* __restrict__ partial, int splits, int64_t n,
+                                                       G* __restrict__ dbias) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    float s = 0.0f;
+    for (int j = 0; j < splits; ++j) s += partial[(size_t)j * n + i];
+    mm_st(dbias + i, s);
+}
+
+template <typename T>
+hipError_t dz_launch(const MmArgs& a, T* dz, hipStream_t s) {
+    const bool glu = a.act == MM_SWIGLU;
+    const int cols = glu ? a.N / 2 : a.N;
+    const dim3 g((uint32_t)((cols + DZ_COLS - 1) / DZ_COLS), (uint32_t)a.splits, (uint32_t)a.E);
+    if (glu)
+        mm_dz_kernel<T, true><<<g, 256, 0, s>>>(a, dz);
+    else
+        mm_dz_kernel<T, false><<<g, 256, 0, s>>>(a, dz);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mm_plan(const MmArgs& a, int chunk_rows, MmChunk* chunks, int32_t* n_chunks, hipStream_t s) {
+    mm_plan_kernel<<<1, 1024, 0, s>>>(a.offsets, a.E, a.P, chunk_rows, chunks, n_chunks, a.max_chunks);
+    return hipGetLastError();
+}
+
+hipError_t launch_mm_dz(const MmArgs& a, bool f32, void* dz, hipStream_t s) {
+    hipError_t e = f32 ? dz_launch(a, static_cast<float*>(dz), s) : dz_launch(a, static_cast<uint16_t*>(dz), s);
+    if (e != hipSuccess || !a.dbias) return e;
+    const int64_t n = (int64_t)a.E * a.N;
+    const uint32_t g = (uint32_t)((n + 255) / 256);
+    if (a.grad_f32 || f32)
+        mm_dbias_kernel<float><<<g, 256, 0, s>>>(a.partial, a.splits, n, static_cast<float*>(a.dbias));
+    else
+        mm_dbias_kernel<uint16_t><<<g, 256, 0, s>>>(a.partial, a.splits, n, static_cast<uint16_t*>(a.dbias));
+    return hipGetLastError();
+}
+
+}  // namespace ds4

@@ -290,6 +290,104 @@ int ds4moe_dequantize(int32_t wfmt, const void* data, const void* scales, int64_
 int ds4moe_quantize_mxfp8(const void* x_bf16, int64_t n, uint8_t* codes, uint8_t* scales,
                           void* stream);
 
+/* ---- products at original precision ---------------------------------------
+ * Matrix products of rows with bf16 or fp32 weights, dense (ds4moe_linear) or
+ * grouped by expert with ragged sizes (ds4moe_grouped_matmul), with their
+ * gradients.  The pages keep everything but the routed experts at original
+ * precision (hysenlabs "DwarfStar実地分析", section
+ * "GGUFの対応範囲は意図的に狭い"); these calls compute such projections, the
+ * output head, and experts that are kept in bf16 or fp32 themselves.
+ *
+ * Forward, for row r of group e (w_e: [out_dim][in_dim]):
+ *     z[r][n] = sum_k x[src(r)][k] * w_e[n][k] + bias_e[n]
+ *     y[r]    = act(z[r]) + residual[r]
+ * Backward, from dy = the gradient of y (residual's gradient is dy itself):
+ *     dz[r]       = dy[r] * act'(z[r])
+ *     dx[r][k]    = sum_n dz[r][n] * w_e[n][k]
+ *     dw_e[n][k]  = sum_{r in e} dz[r][n] * x[src(r)][k]
+ *     dbias_e[n]  = sum_{r in e} dz[r][n]
+ * dx has one row for each row r (not for each row of x): where several rows
+ * read the same row of x, their dx rows are still to be summed, which
+ * ds4moe_combine does with topk_w = 1.
+ *
+ * act:  NONE, RELU, SILU (z sigmoid z), GELU (z Phi(z)), GELU_TANH (its tanh
+ *       form), or SWIGLU: z's first half holds the gates, y[f] = silu(z[f]) *
+ *       z[out_dim/2 + f], so out_dim is even and y, dy, residual have
+ *       out_dim/2 columns.
+ * Types: dtype F32: everything fp32.  BF16: x, w, bias, residual, y, z, dy, dx
+ *       bf16, dw and dbias in grad_dtype (BF16 or F32).  Sums are fp32; z and y
+ *       are each rounded once (y from the unrounded z); the backward pass
+ *       rounds dz to bf16 once, as the operand of the dx and dw products
+ *       (dbias sums it unrounded).
+ * Strides: ldx (x, dx), ldw (w, dw), ldy (y, residual, dy) and ldz (z) are row
+ *       strides in elements, 0 = no gaps; each a whole number of 16 bytes and
+ *       at least the row's length.  Elements between a row's end and its
+ *       stride are never written and may hold anything (reads of a row may
+ *       reach the end of its last 16 bytes, which must be memory of the
+ *       tensor's allocation).  Experts follow one another at
+ *       out_dim * ldw; bias and dbias [groups][out_dim] have no gaps.
+ * Limits: 1 <= in_dim, out_dim <= 2^20, 1 <= groups <= 1024,
+ *       1 <= rows <= 2^24, and rows * in_dim, rows * out_dim and
+ *       out_dim * in_dim each at most 2^36 (else DS4MOE_E_SHAPE).
+ * Outputs must not overlap inputs, except that y may be residual itself. */
+typedef enum {
+    DS4MOE_ACT_NONE = 0, DS4MOE_ACT_RELU = 1, DS4MOE_ACT_SILU = 2, DS4MOE_ACT_GELU = 3,
+    DS4MOE_ACT_GELU_TANH = 4, DS4MOE_ACT_SWIGLU = 5
+} ds4moe_act;
+
+typedef struct {
+    int32_t in_dim;      /* K: columns of x                                   */
+    int32_t out_dim;     /* N: rows of a weight matrix, columns of z          */
+    int32_t groups;      /* experts (1 for ds4moe_linear)                     */
+    int32_t dtype;       /* ds4moe_dtype: F32 or BF16                         */
+    int32_t act;         /* ds4moe_act                                        */
+    int32_t grad_dtype;  /* of dw and dbias: F32, or BF16 when dtype is BF16  */
+    int64_t ldx, ldw, ldy, ldz;
+} ds4moe_matmul;
+
+/* y = act(x W^T + bias) + residual for `rows` rows.  bias and residual may be
+ * NULL (none); z may be NULL, or receives the pre-activations that the
+ * backward pass of an activation reads.  workspace: device scratch of
+ * ds4moe_matmul_workspace_bytes(m, rows, 0) bytes (NULL if that is 0). */
+int ds4moe_linear(const ds4moe_matmul* m, int32_t rows, const void* x, const void* w, const void* bias,
+                  const void* residual, void* y, void* z, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/* The gradients of ds4moe_linear.  z: as ds4moe_linear wrote it (NULL for act
+ * NONE).  dx, dw and dbias may each be NULL (not computed; not all three); w
+ * is read for dx only and x for dw only (NULL otherwise allowed).  dw and
+ * dbias are overwritten.  workspace: ds4moe_matmul_workspace_bytes(m, rows, 1). */
+int ds4moe_linear_backward(const ds4moe_matmul* m, int32_t rows, const void* x, const void* w, const void* z,
+                           const void* dy, void* dx, void* dw, void* dbias, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Products grouped by expert.  expert_offsets int32 [groups+1] and sorted_pair
+ * int32 [rows] are those of ds4moe_permute (rows = T*k): rows offsets[e] ..
+ * offsets[e+1]-1 go through expert e, any number from none to all of them;
+ * row r reads x row sorted_pair[r] / top_k of x_rows rows, or x row r when
+ * sorted_pair is NULL (then x_rows = rows and top_k is ignored).  The
+ * products of the gate and up matrices read tokens through sorted_pair; the
+ * down product's rows are in order, and ds4moe_combine takes its y.  Rows
+ * outside every expert's range are left as they were.  Offsets that are not
+ * ascending within [0, rows] leave their expert without rows, and a pair id
+ * outside [0, x_rows * top_k) reads some row of x: the result is then
+ * undefined, but nothing outside the tensors is touched. */
+int ds4moe_grouped_matmul(const ds4moe_matmul* m, int32_t rows, const void* x, int32_t x_rows, const void* w,
+                          const void* bias, const int32_t* expert_offsets, const int32_t* sorted_pair,
+                          int32_t top_k, void* y, void* z, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* The gradients of ds4moe_grouped_matmul, as ds4moe_linear_backward; dw and
+ * dbias of an expert without rows are zero. */
+int ds4moe_grouped_matmul_backward(const ds4moe_matmul* m, int32_t rows, const void* x, int32_t x_rows,
+                                   const void* w, const void* z, const void* dy, const int32_t* expert_offsets,
+                                   const int32_t* sorted_pair, int32_t top_k, void* dx, void* dw, void* dbias,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of the four calls above for up to `rows` rows: forward (0)
+ * or backward (1).  0 on invalid arguments, and where none is needed. */
+size_t ds4moe_matmul_workspace_bytes(const ds4moe_matmul* m, int32_t rows, int32_t backward);
+
 /* Kernel stages, for per-stage timing. */
 typedef enum {
     DS4MOE_STAGE_ROUTE = 0,     /* router top-k kernel                        */
