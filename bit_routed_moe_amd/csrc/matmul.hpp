@@ -155,4 +155,10 @@ __device__ __forceinline__ void mm_out_glu(const MmArgs& a, int e, int r, int f,
     mm_st(static_cast<T*>(a.y) + o, v);
 }
 
+// bf16 tile kernels (matmul_tile.hip).
+int mt_chunk_rows(int P, int E);
+hipError_t launch_mt_forward(const MmArgs& a, hipStream_t s);
+hipError_t launch_mt_dgrad(const MmArgs& a, hipStream_t s);
+hipError_t launch_mt_wgrad(const MmArgs& a, hipStream_t s);
+
 }  // namespace ds4

@@ -156,7 +156,7 @@ int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 }  // namespace
 
-int mm_chunk_rows(bool, int, int, int, int, int) { return MS_T; }
+int mm_chunk_rows(bool f32, int, int P, int, int, int E) { return f32 ? MS_T : mt_chunk_rows(P, E); }
 
 hipError_t launch_mm_forward(const MmArgs& a, bool f32, hipStream_t s) {
     const int tm = a.chunks ? a.max_chunks : cdiv(a.P, MS_T), tn = cdiv(a.N, MS_T);
@@ -164,7 +164,7 @@ hipError_t launch_mm_forward(const MmArgs& a, bool f32, hipStream_t s) {
     if (f32)
         ms_kernel<float, MM_FWD, float><<<g, 256, 0, s>>>(a, tm, tn);
     else
-        ms_kernel<uint16_t, MM_FWD, uint16_t><<<g, 256, 0, s>>>(a, tm, tn);
+        return launch_mt_forward(a, s);
     return hipGetLastError();
 }
 
@@ -174,7 +174,7 @@ hipError_t launch_mm_dgrad(const MmArgs& a, bool f32, hipStream_t s) {
     if (f32)
         ms_kernel<float, MM_DGRAD, float><<<g, 256, 0, s>>>(a, tm, tn);
     else
-        ms_kernel<uint16_t, MM_DGRAD, uint16_t><<<g, 256, 0, s>>>(a, tm, tn);
+        return launch_mt_dgrad(a, s);
     return hipGetLastError();
 }
 
@@ -183,10 +183,8 @@ hipError_t launch_mm_wgrad(const MmArgs& a, bool f32, hipStream_t s) {
     const dim3 g((uint32_t)(tm * tn), (uint32_t)a.E);
     if (f32)
         ms_kernel<float, MM_WGRAD, float><<<g, 256, 0, s>>>(a, tm, tn);
-    else if (a.grad_f32)
-        ms_kernel<uint16_t, MM_WGRAD, float><<<g, 256, 0, s>>>(a, tm, tn);
     else
-        ms_kernel<uint16_t, MM_WGRAD, uint16_t><<<g, 256, 0, s>>>(a, tm, tn);
+        return launch_mt_wgrad(a, s);
     return hipGetLastError();
 }
 

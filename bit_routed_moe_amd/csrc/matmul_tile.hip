@@ -1,0 +1,432 @@
+// bf16 products at original precision on the matrix cores
+// (v_mfma_f32_16x16x32_bf16, fp32 accumulation), for forward, dgrad and wgrad.
+//
+// Every mode is C[row][col] = sum_k R(row, k) Q(col, k), where an operand is
+// either contiguous along the contraction (x and w forward, dz in dgrad) or
+// along the tile (w in dgrad, dz and x in wgrad):
+//   forward  rows: token rows (gathered), cols: weight rows, k: in_dim
+//   dgrad    rows: dz rows,               cols: in_dim,      k: out_dim
+//   wgrad    rows: out_dim,               cols: in_dim,      k: the group's rows
+//
+// A workgroup computes BR x BC outputs in stages of 64 contraction columns,
+// which global_load_lds_dwordx4 brings into a ring of LDS buffers without
+// passing through registers.  One barrier per stage: after it the stage has
+// landed for every wave and every wave is done with the one before, whose
+// buffer the next request fills.
+//   Contiguous along k: tile row r is 128 bytes, its 16-byte chunk c in slot
+//     c ^ ((r >> 1) & 7), so a fragment read (16 rows at one chunk per lane
+//     quarter, ds_read_b128) covers all 64 banks.
+//   Contiguous along the tile: contraction row k is one LDS row, its 32-byte
+//     granule g (16 columns) in place g ^ (k & 3 | (k >> 3 & 1) << 2); the
+//     fragment is read transposed (ds_read_b64_tr_b16: 16 lanes take 4
+//     contraction rows x 16 columns, and a lane gets its column's 4 values).
+// The column operand goes first into the matrix instruction, so a lane holds 4
+// consecutive columns of one row of C; they leave through LDS in whole rows.
+#include "matmul.hpp"
+
+namespace ds4 {
+
+namespace {
+
+constexpr int MT_K = 64;   // contraction columns per stage
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+// 64 lanes x 16 bytes from global memory into LDS at lds_dst + 16 * lane.
+// Inline asm, so that the compiler's wait counts leave the LDS reads alone;
+// the stage loop waits explicitly.
+__device__ __forceinline__ void mt_dma16(const void* g, uint32_t lds_dst) {
+    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_dst);
+    asm volatile(
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %0, off"
+        :
+        : "v"(g), "s"(m0)
+        : "memory", "m0");
+}
+
+// Wait until at most N of this wave's vector-memory operations are outstanding.
+template <int N>
+__device__ __forceinline__ void mt_wait_vm() {
+    static_assert(N >= 0 && N < 64, "vmcnt is 6 bits");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Workgroup barrier behind this wave's finished LDS reads.
+__device__ __forceinline__ void mt_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Tile t of tr x tc tiles: groups of 8 row tiles, row tiles first inside a
+// group, so that tiles that run together share operands in their L2.
+__device__ __forceinline__ void mt_tile(int t, int tr, int tc, int& r, int& c) {
+    const int sg = t / (8 * tc), rem = t - sg * (8 * tc);
+    const int rows = min(8, tr - 8 * sg);
+    c = rem / rows;
+    r = 8 * sg + rem - c * rows;
+}
+
+// One operand of BT tile rows (or columns) staged by NW waves.
+template <bool STRIDED, int BT, int NW>
+struct MtOperand {
+    static constexpr int BYTES = BT * MT_K * 2;
+    static constexpr int ND = BYTES / 1024 / NW;   // DMAs per wave and stage
+    static_assert(ND * NW * 1024 == BYTES, "whole DMAs per wave");
+    static constexpr int CPR = STRIDED ? BT / 8 : 8;   // 16-byte chunks per LDS row
+    static constexpr int RPD = 64 / CPR;               // LDS rows per DMA
+
+    // LDS row and chunk that DMA i of wave w brings for this lane
+    static __device__ __forceinline__ int lds_row(int i, int w, int lane) { return (i * NW + w) * RPD + lane / CPR; }
+    static __device__ __forceinline__ int chunk(int row, int lane) {
+        const int s = lane % CPR;
+        if constexpr (STRIDED) return s ^ (((row & 3) | ((row >> 1) & 4)) << 1);
+        return s ^ ((row >> 1) & 7);
+    }
+    // Fragment t (16 tile rows from t0 + 16 * t on) of k-step ks.
+    static __device__ __forceinline__ bf16x8 frag(const uint8_t* buf, int t0, int t, int ks, int lane) {
+        const int m = lane & 15, q = lane >> 4;
+        if constexpr (STRIDED) {
+            const int f = (m >> 2) | ((q & 1) << 2);
+            const int g = (t0 >> 4) + t;
+            const uint8_t* p = buf + (ks * 32 + 8 * q + (m >> 2)) * (BT * 2) + ((g ^ f) << 5) + (m & 3) * 8;
+            typedef __attribute__((address_space(3))) s16x4 lds4;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 4 * BT * 2));
+            return __builtin_bit_cast(bf16x8, s16x8(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)));
+        } else {
+            const int r = t0 + 16 * t + m;
+            return *reinterpret_cast<const bf16x8*>(buf + r * 128 + (((ks * 4 + q) ^ (m >> 1)) << 4));
+        }
+    }
+    // Zeros from contraction column krem of the stage on.
+    static __device__ __forceinline__ void clear_tail(uint8_t* buf, int krem, int tid) {
+        if constexpr (STRIDED) {
+            for (int i = krem * (BT / 8) + tid; i < MT_K * (BT / 8); i += NW * 64)
+                *reinterpret_cast<u32x4*>(buf + i * 16) = u32x4{0, 0, 0, 0};
+        } else {
+            for (int i = tid; i < BT * 8; i += NW * 64) {
+                const int r = i >> 3, c = i & 7;
+                uint8_t* p = buf + r * 128 + ((c ^ ((r >> 1) & 7)) << 4);
+                if (8 * c >= krem)
+                    *reinterpret_cast<u32x4*>(p) = u32x4{0, 0, 0, 0};
+                else
+                    for (int j = krem - 8 * c; j < 8; ++j) reinterpret_cast<uint16_t*>(p)[j] = 0;
+            }
+        }
+    }
+};
+
+// 8 values of a row (vec: the address is 16-byte aligned and all 8 exist).
+__device__ __forceinline__ void mt_st8(uint16_t* p, const float (&v)[8], int n, bool vec) {
+    if (vec) {
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        *reinterpret_cast<u32x4*>(p) = o;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = (uint16_t)f32_to_bf16(v[i]);
+    }
+}
+__device__ __forceinline__ void mt_st8(float* p, const float (&v)[8], int n, bool vec) {
+    if (vec) {
+        reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
+        reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = v[i];
+    }
+}
+__device__ __forceinline__ void mt_add8(float (&v)[8], const uint16_t* p, int n, bool vec) {
+    if (vec) {
+        const u32x4 o = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] += __uint_as_float(o[i] << 16);
+            v[2 * i + 1] += __uint_as_float(o[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) v[i] += bf16_to_f32(p[i]);
+    }
+}
+
+// A wave's outputs pass through its own LDS region on their way out, so that
+// the activation code exists once and rows leave in whole 16-byte pieces:
+// rows of CW floats, 16-byte chunk c of row r at c ^ (r & 15).
+template <int CW>
+__device__ __forceinline__ void mt_get8(const uint8_t* reg, int r, int col, float (&v)[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(reg + r * (CW * 4) + ((((col >> 2) + h) ^ (r & 15)) << 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * h + i] = x[i];
+    }
+}
+
+// Forward epilogue of 8 columns from n on (cnt of them exist) of row r.
+__device__ __forceinline__ void mt_out8(const MmArgs& a, const uint16_t* bias, int r, int n, int cnt, float (&v)[8]) {
+    const bool vec = cnt >= 8;
+    if (bias) mt_add8(v, bias + n, cnt, vec && (a.N & 7) == 0);
+    if (a.z) mt_st8(static_cast<uint16_t*>(a.z) + (size_t)r * a.ldz + n, v, cnt, vec);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = mm_act(v[i], a.act);
+    const size_t o = (size_t)r * a.ldy + n;
+    if (a.residual) mt_add8(v, static_cast<const uint16_t*>(a.residual) + o, cnt, vec);
+    mt_st8(static_cast<uint16_t*>(a.y) + o, v, cnt, vec);
+}
+
+__device__ __forceinline__ void mt_out8_glu(const MmArgs& a, const uint16_t* bias, int r, int f, int cnt,
+                                            float (&g)[8], float (&u)[8]) {
+    const int half = a.N >> 1;
+    const bool vec = cnt >= 8, vecu = vec && (half & 7) == 0;
+    if (bias) {
+        mt_add8(g, bias + f, cnt, vecu);   // (expert rows of an odd N start anywhere)
+        mt_add8(u, bias + half + f, cnt, vecu);
+    }
+    if (a.z) {
+        uint16_t* zr = static_cast<uint16_t*>(a.z) + (size_t)r * a.ldz;
+        mt_st8(zr + f, g, cnt, vec);
+        mt_st8(zr + half + f, u, cnt, vecu);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = g[i] / (1.0f + expf(-g[i])) * u[i];
+    const size_t o = (size_t)r * a.ldy + f;
+    if (a.residual) mt_add8(g, static_cast<const uint16_t*>(a.residual) + o, cnt, vec);
+    mt_st8(static_cast<uint16_t*>(a.y) + o, g, cnt, vec);
+}
+
+// WR x WC waves, each (BR / WR) x (BC / WC) outputs; ST stage buffers.
+template <int MODE, int BR, int BC, int WR, int WC, int ST, typename G>
+__global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int tc) {
+    constexpr int NW = WR * WC;
+    using RowOp = MtOperand<MODE == MM_WGRAD, BR, NW>;
+    using ColOp = MtOperand<MODE != MM_FWD, BC, NW>;
+    constexpr int STB = RowOp::BYTES + ColOp::BYTES;
+    constexpr int MI = BR / WR / 16, NI = BC / WC / 16;
+    constexpr int LPS = RowOp::ND + ColOp::ND;   // DMAs per wave and stage
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[ST * STB];
+    const uint32_t lds32 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    // this workgroup's tile: each of the 8 XCDs (workgroup id modulo 8) takes
+    // a contiguous eighth of the tiles that exist
+    int ntr = tr;
+    if (MODE != MM_WGRAD && a.chunks) ntr = a.n_chunks[0];
+    const int total = ntr * tc, per = (total + 7) >> 3, slot = (int)blockIdx.x >> 3;
+    const int t = ((int)blockIdx.x & 7) * per + slot;
+    if (slot >= per || t >= total) return;
+    int rt, ct;
+    mt_tile(t, ntr, tc, rt, ct);
+    const int c0 = ct * BC;
+    int r0 = 0, kdim;
+    MmChunk ch;
+    if constexpr (MODE == MM_WGRAD) {
+        ch.group = blockIdx.y;
+        mm_group_rows(a.offsets, ch.group, a.P, ch.row0, ch.n);
+        r0 = rt * BR;
+        kdim = ch.n;
+    } else {
+        if (!mm_chunk(a, rt, BR, ch)) return;
+        kdim = MODE == MM_FWD ? a.K : a.N;
+    }
+    const bool glu = MODE == MM_FWD && a.act == MM_SWIGLU;
+    const uint16_t* x = static_cast<const uint16_t*>(a.x);
+    const uint16_t* dz = static_cast<const uint16_t*>(a.dz);
+    const uint16_t* wg = static_cast<const uint16_t*>(a.w) + (size_t)ch.group * a.N * a.ldw;
+
+    // fixed part of each DMA's source address
+    const uint16_t* rsrc[RowOp::ND];
+    const uint16_t* csrc[ColOp::ND];
+    int pair[ColOp::ND];   // wgrad: x rows of the next stage (sorted_pair entries)
+#pragma unroll
+    for (int i = 0; i < RowOp::ND; ++i) {
+        const int lr = RowOp::lds_row(i, w, lane);
+        if constexpr (MODE == MM_FWD)
+            rsrc[i] = x + (size_t)mm_src(a, ch.row0 + min(lr, ch.n - 1)) * a.ldx;
+        else if constexpr (MODE == MM_DGRAD)
+            rsrc[i] = dz + (size_t)(ch.row0 + min(lr, ch.n - 1)) * a.lddz;
+        else
+            rsrc[i] = dz + (size_t)ch.row0 * a.lddz + 8 * min(r0 / 8 + RowOp::chunk(lr, lane), (a.N - 1) / 8);
+    }
+#pragma unroll
+    for (int i = 0; i < ColOp::ND; ++i) {
+        const int lr = ColOp::lds_row(i, w, lane);
+        if constexpr (MODE == MM_FWD) {
+            const int n = mm_col(a, glu, c0, lr);
+            csrc[i] = wg + (size_t)(n < 0 ? a.N - 1 : n) * a.ldw;
+        } else {
+            csrc[i] = (MODE == MM_DGRAD ? wg : x) + 8 * min(c0 / 8 + ColOp::chunk(lr, lane), (a.K - 1) / 8);
+        }
+    }
+    const int kchunk = (kdim - 1) / 8;
+    auto load_pairs = [&](int st) {
+        if constexpr (MODE == MM_WGRAD) {
+            if (a.sorted_pair) {
+#pragma unroll
+                for (int i = 0; i < ColOp::ND; ++i)
+                    pair[i] = a.sorted_pair[ch.row0 + min(st * MT_K + ColOp::lds_row(i, w, lane), kdim - 1)];
+            }
+        }
+    };
+    auto issue = [&](int st) {
+        const uint32_t buf = lds32 + (uint32_t)(st % ST) * STB;
+#pragma unroll
+        for (int i = 0; i < RowOp::ND; ++i) {
+            const int lr = RowOp::lds_row(i, w, lane);
+            const uint16_t* p;
+            if constexpr (MODE == MM_WGRAD)
+                p = rsrc[i] + (size_t)min(st * MT_K + lr, kdim - 1) * a.lddz;
+            else
+                p = rsrc[i] + 8 * min(st * (MT_K / 8) + RowOp::chunk(lr, lane), kchunk);
+            mt_dma16(p, buf + (uint32_t)(i * NW + w) * 1024u);
+        }
+#pragma unroll
+        for (int i = 0; i < ColOp::ND; ++i) {
+            const int lr = ColOp::lds_row(i, w, lane);
+            const uint16_t* p;
+            if constexpr (MODE == MM_FWD) {
+                p = csrc[i] + 8 * min(st * (MT_K / 8) + ColOp::chunk(lr, lane), kchunk);
+            } else if constexpr (MODE == MM_DGRAD) {
+                p = csrc[i] + (size_t)min(st * MT_K + lr, kdim - 1) * a.ldw;
+            } else {
+                int s = ch.row0 + min(st * MT_K + lr, kdim - 1);
+                if (a.sorted_pair)
+                    s = min((int)((uint32_t)pair[i] / (uint32_t)a.top_k), a.x_rows - 1);
+                p = csrc[i] + (size_t)s * a.ldx;
+            }
+            mt_dma16(p, buf + RowOp::BYTES + (uint32_t)(i * NW + w) * 1024u);
+        }
+    };
+
+    f32x4 acc[NI][MI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < MI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int wr0 = (w % WR) * (BR / WR), wc0 = (w / WR) * (BC / WC);
+    const int ns = (kdim + MT_K - 1) / MT_K;
+    static_assert(ST == 2 || MODE != MM_WGRAD, "the pair loads are counted in two-stage waits only");
+    if (ns > 0) {
+        load_pairs(0);
+#pragma unroll
+        for (int s = 0; s < ST - 1; ++s)
+            if (s < ns) issue(s);
+        load_pairs(1);
+    }
+    for (int st = 0; st < ns; ++st) {
+        if (ST > 2 && st + ST - 2 < ns)
+            mt_wait_vm<(ST - 2) * LPS>();
+        else
+            mt_wait_vm<0>();
+        mt_barrier();
+        if (st + ST - 1 < ns) {
+            issue(st + ST - 1);
+            load_pairs(st + ST);
+        }
+        uint8_t* buf = lds + (st % ST) * STB;
+        if (st == ns - 1 && kdim % MT_K) {
+            RowOp::clear_tail(buf, kdim % MT_K, tid);
+            ColOp::clear_tail(buf + RowOp::BYTES, kdim % MT_K, tid);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int ks = 0; ks < MT_K / 32; ++ks) {
+            bf16x8 rf[MI], cf[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) cf[i] = ColOp::frag(buf + RowOp::BYTES, wc0, i, ks, lane);
+#pragma unroll
+            for (int j = 0; j < MI; ++j) rf[j] = RowOp::frag(buf, wr0, j, ks, lane);
+#pragma unroll
+            for (int j = 0; j < MI; ++j)
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cf[i], rf[j], acc[i][j], 0, 0, 0);
+        }
+    }
+
+    // Out through LDS, RP rows of the wave's tile at a time.  In the
+    // accumulators a lane holds columns 4q .. 4q+3 of row m of each 16 x 16
+    // block.
+    constexpr int CW = BC / WC, WROWS = BR / WR;
+    constexpr int RP = ST * STB / NW / (CW * 4) >= WROWS ? WROWS : ST * STB / NW / (CW * 4) / 16 * 16;
+    static_assert(RP >= 16 && WROWS % RP == 0 && CW == 64, "passes of whole row tiles");
+    const uint16_t* bias = nullptr;
+    if (MODE == MM_FWD && a.bias) bias = static_cast<const uint16_t*>(a.bias) + (size_t)ch.group * a.N;
+    const int rows = MODE == MM_WGRAD ? a.N - r0 : ch.n;
+    uint8_t* reg = lds + w * (RP * CW * 4);
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < WROWS / RP; ++p) {
+        const int m = lane & 15, q = lane >> 4;
+#pragma unroll
+        for (int j = 0; j < RP / 16; ++j)
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                *reinterpret_cast<f32x4*>(reg + (16 * j + m) * (CW * 4) + (((4 * i + q) ^ m) << 4)) =
+                    acc[i][p * (RP / 16) + j];
+        const int rbase = wr0 + p * RP;
+        if (MODE == MM_FWD && glu) {
+            // 16 gate columns, then the 16 up columns they pair with
+            const int c8 = lane & 3, col = 32 * (c8 >> 1) + 8 * (c8 & 1);
+            const int f = ((c0 + wc0) >> 1) + 8 * c8, cnt = (a.N >> 1) - f;
+#pragma unroll 1
+            for (int rr = lane >> 2; rr < RP; rr += 16) {
+                float g[8], u[8];
+                mt_get8<CW>(reg, rr, col, g);
+                mt_get8<CW>(reg, rr, col + 16, u);
+                if (rbase + rr < rows && cnt > 0) mt_out8_glu(a, bias, ch.row0 + rbase + rr, f, cnt, g, u);
+            }
+        } else {
+            const int col = 8 * (lane & 7), n = c0 + wc0 + col, cnt = (MODE == MM_FWD ? a.N : a.K) - n;
+#pragma unroll 1
+            for (int rr = lane >> 3; rr < RP; rr += 8) {
+                float v[8];
+                mt_get8<CW>(reg, rr, col, v);
+                if (rbase + rr >= rows || cnt <= 0) continue;
+                if constexpr (MODE == MM_FWD) {
+                    mt_out8(a, bias, ch.row0 + rbase + rr, n, cnt, v);
+                } else {
+                    G* o = MODE == MM_DGRAD ? static_cast<G*>(a.dx) + (size_t)(ch.row0 + rbase + rr) * a.ldx
+                                            : static_cast<G*>(a.dw) + ((size_t)ch.group * a.N + r0 + rbase + rr) * a.ldw;
+                    mt_st8(o + n, v, cnt, cnt >= 8);
+                }
+            }
+        }
+    }
+}
+
+int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+template <int MODE, int BR, int BC, int WR, int WC, int ST, typename G>
+hipError_t mt_launch(const MmArgs& a, hipStream_t s) {
+    const int tr = MODE == MM_WGRAD ? cdiv(a.N, BR) : (a.chunks ? a.max_chunks : cdiv(a.P, BR));
+    const int tc = cdiv(MODE == MM_FWD ? a.N : a.K, BC);
+    const int64_t total = (int64_t)tr * tc;
+    const dim3 g((uint32_t)((total + 7) / 8 * 8), MODE == MM_WGRAD ? (uint32_t)a.E : 1u);
+    mt_kernel<MODE, BR, BC, WR, WC, ST, G><<<g, 64 * WR * WC, 0, s>>>(a, tr, tc);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int mt_chunk_rows(int P, int E) { return P / E <= 160 ? 128 : 256; }
+
+hipError_t launch_mt_forward(const MmArgs& a, hipStream_t s) {
+    if (mt_chunk_rows(a.P, a.E) == 128) return mt_launch<MM_FWD, 128, 256, 2, 4, 3, uint16_t>(a, s);
+    return mt_launch<MM_FWD, 256, 256, 2, 4, 2, uint16_t>(a, s);
+}
+
+hipError_t launch_mt_dgrad(const MmArgs& a, hipStream_t s) {
+    if (mt_chunk_rows(a.P, a.E) == 128) return mt_launch<MM_DGRAD, 128, 256, 2, 4, 3, uint16_t>(a, s);
+    return mt_launch<MM_DGRAD, 256, 256, 2, 4, 2, uint16_t>(a, s);
+}
+
+hipError_t launch_mt_wgrad(const MmArgs& a, hipStream_t s) {
+    if (a.grad_f32) return mt_launch<MM_WGRAD, 256, 256, 2, 4, 2, float>(a, s);
+    return mt_launch<MM_WGRAD, 256, 256, 2, 4, 2, uint16_t>(a, s);
+}
+
+}  // namespace ds4
