@@ -18,7 +18,7 @@ __all__ = [
     "workspace_bytes", "workspace_region", "WS_REGION", "dequantize", "quantize_mxfp8", "status_string", "version",
     "EXPORTS", "STAGE", "set_stage_events",
     "ACT", "Matmul", "make_matmul", "matmul_workspace_bytes", "linear", "linear_backward", "grouped_matmul",
-    "grouped_matmul_backward",
+    "grouped_matmul_backward", "sample", "sample_workspace_bytes",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libds4moe.so")
@@ -35,7 +35,7 @@ EXPORTS = (
     "ds4moe_version", "ds4moe_set_stage_events", "ds4moe_forward_path", "ds4moe_quantize_mxfp8",
     "ds4moe_workspace_region", "ds4moe_forward_noalloc", "ds4moe_forward_noalloc_max_bytes",
     "ds4moe_linear", "ds4moe_linear_backward", "ds4moe_grouped_matmul", "ds4moe_grouped_matmul_backward",
-    "ds4moe_matmul_workspace_bytes",
+    "ds4moe_matmul_workspace_bytes", "ds4moe_sample", "ds4moe_sample_workspace_bytes",
 )
 
 WS_REGION = {"topk_idx": 0, "topk_w": 1, "offsets": 2, "sorted_pair": 3, "pair_pos": 4, "active": 5,
@@ -100,6 +100,8 @@ def _load():
         "ds4moe_grouped_matmul": (i32, [mmp, i32, vp, i32, vp, vp, vp, vp, i32, vp, vp, vp, sz, vp]),
         "ds4moe_grouped_matmul_backward": (i32, [mmp, i32, vp, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]),
         "ds4moe_matmul_workspace_bytes": (sz, [mmp, i32, i32]),
+        "ds4moe_sample": (i32, [i32, i32, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "ds4moe_sample_workspace_bytes": (sz, [i32, i32]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -295,3 +297,23 @@ def grouped_matmul_backward(m, rows, x, w, expert_offsets, dy, z=None, sorted_pa
     xr = x_rows if x_rows is not None else (x.shape[0] if x is not None else rows)
     _check(lib.ds4moe_grouped_matmul_backward(ctypes.byref(m), rows, px, xr, pw, pz, pdy, po, pp, top_k, pdx, pdw,
                                               pdb, ps, _ws(workspace), _s(stream)))
+
+
+# ---- token sampling ------------------------------------------------------------
+
+def sample_workspace_bytes(B: int, V: int) -> int:
+    return int(lib.ds4moe_sample_workspace_bytes(B, V))
+
+
+def sample(B, V, logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, prob=None, workspace=None,
+           stream=None):
+    """token[B] (and prob[B]) sampled from logits [B][V] (fp32 or bf16; rows may
+    be logits.stride(0) apart) with the random numbers u[B]; the filters' values
+    are per row, None switches one off."""
+    import torch
+    dtype = {torch.float32: 0, torch.bfloat16: 1}.get(logits.dtype)
+    if dtype is None or logits.stride(-1) != 1:
+        raise Ds4MoeError(-1, f"logits {logits.dtype} with strides {logits.stride()}")
+    pl, pt, pk, pp, pm, pu, po, pr, ps = _d(logits, temperature, top_k, top_p, min_p, u, token, prob, workspace)
+    _check(lib.ds4moe_sample(B, V, pl, logits.stride(0) if B > 1 else V, dtype, pt, pk, pp, pm, pu, po, pr, ps,
+                             _ws(workspace), _s(stream)))

@@ -839,4 +839,30 @@ int ds4moe_grouped_matmul_backward(const ds4moe_matmul* m, int32_t rows, const v
     return mm_backward(m, a, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
 }
 
+size_t ds4moe_sample_workspace_bytes(int32_t, int32_t) { return 0; }
+
+int ds4moe_sample(int32_t B, int32_t V, const void* logits, int64_t ld, int32_t dtype, const float* temperature,
+                  const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* token,
+                  float* prob, void* workspace, size_t workspace_bytes, void* stream) {
+    if (dtype != DS4MOE_DT_F32 && dtype != DS4MOE_DT_BF16) {
+        if (dtype == DS4MOE_DT_FP8_E4M3) return fail(DS4MOE_E_UNSUPPORTED, "fp8 logits");
+        return fail(DS4MOE_E_ARG, "dtype %d", dtype);
+    }
+    if (B < 1 || B > 65536) return fail(DS4MOE_E_SHAPE, "B %d not in [1, 65536]", B);
+    if (V < 1 || V > (1 << 20)) return fail(DS4MOE_E_SHAPE, "V %d not in [1, 2^20]", V);
+    if (ld < V || ld > ((int64_t)1 << 31)) return fail(DS4MOE_E_SHAPE, "ld %lld for rows of %d", (long long)ld, V);
+    REQ_PTR(logits);
+    OPT_PTR(temperature);
+    OPT_PTR(top_k);
+    OPT_PTR(top_p);
+    OPT_PTR(min_p);
+    REQ_PTR(u);
+    REQ_PTR(token);
+    OPT_PTR(prob);
+    TRY(check_workspace(workspace, workspace_bytes, ds4moe_sample_workspace_bytes(B, V)));
+    return hip_status(ds4::launch_sample(B, V, ld, dtype == DS4MOE_DT_F32, logits, temperature, top_k, top_p, min_p, u,
+                                         token, prob, static_cast<hipStream_t>(stream)),
+                      "sample");
+}
+
 }  // extern "C"

@@ -388,6 +388,42 @@ int ds4moe_grouped_matmul_backward(const ds4moe_matmul* m, int32_t rows, const v
  * or backward (1).  0 on invalid arguments, and where none is needed. */
 size_t ds4moe_matmul_workspace_bytes(const ds4moe_matmul* m, int32_t rows, int32_t backward);
 
+/* Token sampling from logits, one given random number per row: for each row r
+ * of B, over V tokens in (logit descending, index ascending) order with
+ * weights w_i = exp((logit_i - max) / temperature[r]),
+ *   1. top-k: the first top_k[r] tokens stay (<= 0: all);
+ *   2. top-p: of those, the shortest prefix whose weights reach top_p[r] of
+ *      their sum, at least one token (>= 1: all);
+ *   3. min-p: of those, the tokens with w_i >= min_p[r] (<= 0: all), that is
+ *      with at least min_p times the likeliest token's probability; the first
+ *      token always stays;
+ *   4. token[r] = the first token at which the running sum of the kept weights
+ *      exceeds u[r] times their total, u in [0, 1) (values outside count as
+ *      the nearest inside); prob[r] = its weight over that total.
+ * temperature <= 0 (or NaN) is the greedy choice: the largest logit, lowest
+ * index first (-0 == +0), with prob 1.  Logits that are -infinity or NaN are
+ * never chosen; a row of nothing else has token -1 and prob 0.  A row with
+ * logits of +infinity chooses among those.
+ * The pages' engine samples on the coordinator after the last layer (qiita
+ * "DwarfStar の TCP パイプライン分散推論を読む", section 9) and has a
+ * temperature flag; the filters and their order are this library's reading.
+ * Weights are computed in 64 bits and held to 2^-44 of the largest (a token
+ * below that is never chosen), sums exactly, so the choice depends on nothing
+ * but the row's values.
+ * logits [B] rows of V, ld elements apart (ld >= V, any alignment of rows; a
+ * row's last 16-byte piece of memory must belong to the allocation), fp32 or
+ * bf16.  temperature, top_p, min_p fp32 [B] and top_k int32 [B] may each be
+ * NULL (temperature 1, filter off); u fp32 [B]; token int32 [B]; prob fp32 [B]
+ * or NULL.  1 <= B <= 65536, 1 <= V <= 2^20.  workspace: device scratch of
+ * ds4moe_sample_workspace_bytes(B, V) bytes (NULL if that is 0). */
+int ds4moe_sample(int32_t B, int32_t V, const void* logits, int64_t ld, int32_t dtype, const float* temperature,
+                  const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* token,
+                  float* prob, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes that ds4moe_sample needs (0 on invalid sizes, and where none
+ * is needed). */
+size_t ds4moe_sample_workspace_bytes(int32_t B, int32_t V);
+
 /* Kernel stages, for per-stage timing. */
 typedef enum {
     DS4MOE_STAGE_ROUTE = 0,     /* router top-k kernel                        */
