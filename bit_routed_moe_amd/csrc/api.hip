@@ -839,7 +839,10 @@ int ds4moe_grouped_matmul_backward(const ds4moe_matmul* m, int32_t rows, const v
     return mm_backward(m, a, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
 }
 
-size_t ds4moe_sample_workspace_bytes(int32_t, int32_t) { return 0; }
+size_t ds4moe_sample_workspace_bytes(int32_t B, int32_t V) {
+    if (B < 1 || B > 65536 || V < 1 || V > (1 << 20)) return 0;
+    return ds4::sample_workspace_bytes(B, V);
+}
 
 int ds4moe_sample(int32_t B, int32_t V, const void* logits, int64_t ld, int32_t dtype, const float* temperature,
                   const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* token,
@@ -861,7 +864,7 @@ int ds4moe_sample(int32_t B, int32_t V, const void* logits, int64_t ld, int32_t 
     OPT_PTR(prob);
     TRY(check_workspace(workspace, workspace_bytes, ds4moe_sample_workspace_bytes(B, V)));
     return hip_status(ds4::launch_sample(B, V, ld, dtype == DS4MOE_DT_F32, logits, temperature, top_k, top_p, min_p, u,
-                                         token, prob, static_cast<hipStream_t>(stream)),
+                                         token, prob, workspace, static_cast<hipStream_t>(stream)),
                       "sample");
 }
 

@@ -175,6 +175,7 @@ hipError_t launch_mm_dz(const MmArgs& a, bool f32, void* dz, hipStream_t s);
 // Token sampling: rows of V logits ld elements apart (fp32 or bf16).
 hipError_t launch_sample(int B, int V, int64_t ld, bool f32, const void* logits, const float* temperature,
                          const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* token,
-                         float* prob, hipStream_t s);
+                         float* prob, void* workspace, hipStream_t s);
+size_t sample_workspace_bytes(int B, int V);
 
 }  // namespace ds4

@@ -407,9 +407,9 @@ size_t ds4moe_matmul_workspace_bytes(const ds4moe_matmul* m, int32_t rows, int32
  * The pages' engine samples on the coordinator after the last layer (qiita
  * "DwarfStar の TCP パイプライン分散推論を読む", section 9) and has a
  * temperature flag; the filters and their order are this library's reading.
- * Weights are computed in 64 bits and held to 2^-44 of the largest (a token
- * below that is never chosen), sums exactly, so the choice depends on nothing
- * but the row's values.
+ * Weights are computed in 64 bits and held to 2^-43 of the largest (a token
+ * below e^-31 of it is never chosen), sums exactly, so the choice depends on
+ * nothing but the row's values.
  * logits [B] rows of V, ld elements apart (ld >= V, any alignment of rows; a
  * row's last 16-byte piece of memory must belong to the allocation), fp32 or
  * bf16.  temperature, top_p, min_p fp32 [B] and top_k int32 [B] may each be
