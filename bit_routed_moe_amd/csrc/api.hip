@@ -359,12 +359,13 @@ int mm_max_chunks(const ds4moe_matmul* m, int32_t rows, int bm) {
 }
 
 struct MmLayout {
-    size_t plan, dz, partial, total;
+    size_t plan, split, dz, partial, total;
 };
 
-// Workspace of a call (sizes grow with rows: the plan is sized for the
-// smallest chunks).
-MmLayout mm_layout(const ds4moe_matmul* m, int32_t rows, bool backward) {
+// Workspace of a call.  The plan is sized for the smallest chunks.  A split
+// contraction's partial sums come last: `call` gives what these rows take,
+// else a bound that grows with rows (a call with fewer rows may split more).
+MmLayout mm_layout(const ds4moe_matmul* m, int32_t rows, bool backward, bool call) {
     MmLayout L{};
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -380,6 +381,12 @@ MmLayout mm_layout(const ds4moe_matmul* m, int32_t rows, bool backward) {
         L.dz = take(m->act != DS4MOE_ACT_NONE ? (size_t)rows * lddz * (f32 ? 4 : 2) : 0);
         L.partial = take((size_t)mm_splits(m, rows) * m->groups * m->out_dim * 4);
     }
+    // (the launches of a backward pass follow one another, so they share theirs)
+    auto split = [&](int mode) {
+        return ds4::mm_split_bytes(f32, mode, rows, m->in_dim, m->out_dim, m->groups, call);
+    };
+    const size_t sd = split(ds4::MM_DGRAD), sw = split(ds4::MM_WGRAD);
+    L.split = take(!backward ? split(ds4::MM_FWD) : (sd > sw ? sd : sw));
     L.total = align256(off);
     return L;
 }
@@ -429,6 +436,7 @@ int mm_plan(const ds4moe_matmul* m, ds4::MmArgs& a, int mode, void* ws, const Mm
     a.n_chunks = nullptr;
     if (m->groups == 1) return DS4MOE_OK;
     const int bm = ds4::mm_chunk_rows(m->dtype == DS4MOE_DT_F32, mode, a.P, a.K, a.N, a.E);
+    if (bm == 0) return DS4MOE_OK;
     int32_t* n = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + L.plan);
     ds4::MmChunk* c = reinterpret_cast<ds4::MmChunk*>(static_cast<uint8_t*>(ws) + L.plan + 256);
     a.max_chunks = mm_max_chunks(m, a.P, bm);
@@ -460,17 +468,19 @@ int mm_backward_args(const ds4moe_matmul* m, int32_t rows, ds4::MmArgs& a, const
 }
 
 int mm_forward(const ds4moe_matmul* m, ds4::MmArgs& a, void* ws, size_t bytes, hipStream_t s) {
-    const MmLayout L = mm_layout(m, a.P, false);
+    const MmLayout L = mm_layout(m, a.P, false, true);
     TRY(check_workspace(ws, bytes, L.total));
     TRY(mm_plan(m, a, ds4::MM_FWD, ws, L, s));
+    a.kpart = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.split);
     return hip_status(ds4::launch_mm_forward(a, m->dtype == DS4MOE_DT_F32, s), "matmul");
 }
 
 int mm_backward(const ds4moe_matmul* m, ds4::MmArgs& a, void* ws, size_t bytes, hipStream_t s) {
     const bool f32 = m->dtype == DS4MOE_DT_F32;
-    const MmLayout L = mm_layout(m, a.P, true);
+    const MmLayout L = mm_layout(m, a.P, true, true);
     TRY(check_workspace(ws, bytes, L.total));
     a.splits = mm_splits(m, a.P);
+    a.kpart = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.split);
     a.partial = a.dbias ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.partial) : nullptr;
     a.dz = a.dy;
     a.lddz = a.ldy;
@@ -758,7 +768,7 @@ int ds4moe_dequantize(int32_t wfmt, const void* data, const void* scales, int64_
 
 size_t ds4moe_matmul_workspace_bytes(const ds4moe_matmul* m, int32_t rows, int32_t backward) {
     if (check_mm(m, rows) != DS4MOE_OK) return 0;
-    return mm_layout(m, rows, backward != 0).total;
+    return mm_layout(m, rows, backward != 0, false).total;
 }
 
 int ds4moe_linear(const ds4moe_matmul* m, int32_t rows, const void* x, const void* w, const void* bias,

@@ -160,10 +160,19 @@ struct MmArgs {
     bool grad_f32;              // dw and dbias in fp32 (else the rows' type)
     int splits;                 // row splits of the bias gradient
     float* partial;             // [splits][E][N]
+    // splits of the contraction (bf16 tile kernels): fp32 partial sums
+    // [ksplits][rows][ldp], kpart_stride floats apart
+    int ksplits;
+    float* kpart;
+    size_t kpart_stride;
+    int64_t ldp;
 };
 
-// Rows per chunk of the plan that the forward or dgrad launch of these sizes uses.
+// Rows per chunk of the plan that the forward or dgrad launch of these sizes
+// uses (0: no plan).
 int mm_chunk_rows(bool f32, int mode, int P, int K, int N, int E);
+// Scratch of a launch (MmArgs::kpart): for these rows, or a bound for all up to P.
+size_t mm_split_bytes(bool f32, int mode, int P, int K, int N, int E, bool exact);
 // One workgroup lists the chunks of the groups.
 hipError_t launch_mm_plan(const MmArgs& a, int chunk_rows, MmChunk* chunks, int32_t* n_chunks, hipStream_t s);
 hipError_t launch_mm_forward(const MmArgs& a, bool f32, hipStream_t s);

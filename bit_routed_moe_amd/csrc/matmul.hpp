@@ -18,7 +18,7 @@ enum MmAct { MM_NONE = 0, MM_RELU = 1, MM_SILU = 2, MM_GELU = 3, MM_GELU_TANH = 
 enum MmMode { MM_FWD = 0, MM_DGRAD = 1, MM_WGRAD = 2 };
 
 // Smallest rows per chunk that mm_chunk_rows returns (sizes the plan).
-constexpr int MM_MIN_CHUNK = 16;
+constexpr int MM_MIN_CHUNK = 64;
 
 // One piece of a group's rows: forward and dgrad run a row tile of it.
 struct MmChunk {
@@ -156,9 +156,17 @@ __device__ __forceinline__ void mm_out_glu(const MmArgs& a, int e, int r, int f,
 }
 
 // bf16 tile kernels (matmul_tile.hip).
-int mt_chunk_rows(int P, int E);
-hipError_t launch_mt_forward(const MmArgs& a, hipStream_t s);
-hipError_t launch_mt_dgrad(const MmArgs& a, hipStream_t s);
-hipError_t launch_mt_wgrad(const MmArgs& a, hipStream_t s);
+struct MtPick {
+    int shape, splits;
+};
+MtPick mt_pick(int mode, int P, int K, int N, int E);
+int mt_chunk_rows(int mode, int P, int K, int N, int E);
+// Scratch for the partial sums of a split contraction.
+size_t mt_split_bytes(int mode, int P, int K, int N, int E, bool exact);
+hipError_t launch_mt(const MmArgs& a, int mode, hipStream_t s);
+
+// bf16 forward products of few rows (matmul_rows.hip).
+bool mr_takes(int P, int E);
+hipError_t launch_mr_forward(const MmArgs& a, hipStream_t s);
 
 }  // namespace ds4

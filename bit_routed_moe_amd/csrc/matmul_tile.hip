@@ -17,8 +17,8 @@
 //     c ^ ((r >> 1) & 7), so a fragment read (16 rows at one chunk per lane
 //     quarter, ds_read_b128) covers all 64 banks.
 //   Contiguous along the tile: contraction row k is one LDS row, its 32-byte
-//     granule g (16 columns) in place g ^ (k & 3 | (k >> 3 & 1) << 2); the
-//     fragment is read transposed (ds_read_b64_tr_b16: 16 lanes take 4
+//     granule g (16 columns) in place g ^ (k & 3 | (k >> 3 & 1) << 2) (64
+//     columns: g ^ (k >> 1 & 1 | (k >> 3 & 1) << 1)); the fragment is read transposed (ds_read_b64_tr_b16: 16 lanes take 4
 //     contraction rows x 16 columns, and a lane gets its column's 4 values).
 // The column operand goes first into the matrix instruction, so a lane holds 4
 // consecutive columns of one row of C; they leave through LDS in whole rows.
@@ -28,7 +28,10 @@ namespace ds4 {
 
 namespace {
 
-constexpr int MT_K = 64;   // contraction columns per stage
+constexpr int MT_K = 64;            // contraction columns per stage
+constexpr int MT_MAX_SPLITS = 16;   // of the contraction
+// Estimates of mt_pick_, in 64 x 64 x 64 blocks on one CU (about 0.13 us).
+constexpr double MT_START = 20.0, MT_JOIN = 30.0, MT_BYTES = 4e5;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
@@ -74,20 +77,24 @@ struct MtOperand {
     static constexpr int CPR = STRIDED ? BT / 8 : 8;   // 16-byte chunks per LDS row
     static constexpr int RPD = 64 / CPR;               // LDS rows per DMA
 
+    // what a strided operand's granules of LDS row k are moved by
+    static __device__ __forceinline__ int place(int k) {
+        if constexpr (BT >= 128) return (k & 3) | ((k >> 1) & 4);
+        return ((k >> 1) & 1) | ((k >> 2) & 2);   // (two rows per 64 banks)
+    }
     // LDS row and chunk that DMA i of wave w brings for this lane
     static __device__ __forceinline__ int lds_row(int i, int w, int lane) { return (i * NW + w) * RPD + lane / CPR; }
     static __device__ __forceinline__ int chunk(int row, int lane) {
         const int s = lane % CPR;
-        if constexpr (STRIDED) return s ^ (((row & 3) | ((row >> 1) & 4)) << 1);
+        if constexpr (STRIDED) return s ^ (place(row) << 1);
         return s ^ ((row >> 1) & 7);
     }
     // Fragment t (16 tile rows from t0 + 16 * t on) of k-step ks.
     static __device__ __forceinline__ bf16x8 frag(const uint8_t* buf, int t0, int t, int ks, int lane) {
         const int m = lane & 15, q = lane >> 4;
         if constexpr (STRIDED) {
-            const int f = (m >> 2) | ((q & 1) << 2);
-            const int g = (t0 >> 4) + t;
-            const uint8_t* p = buf + (ks * 32 + 8 * q + (m >> 2)) * (BT * 2) + ((g ^ f) << 5) + (m & 3) * 8;
+            const int k = 8 * q + (m >> 2), g = (t0 >> 4) + t;   // (the step's 32 and the half's 4 do not move place)
+            const uint8_t* p = buf + (ks * 32 + k) * (BT * 2) + ((g ^ place(k)) << 5) + (m & 3) * 8;
             typedef __attribute__((address_space(3))) s16x4 lds4;
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p));
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 4 * BT * 2));
@@ -155,12 +162,12 @@ __device__ __forceinline__ void mt_add8(float (&v)[8], const uint16_t* p, int n,
 
 // A wave's outputs pass through its own LDS region on their way out, so that
 // the activation code exists once and rows leave in whole 16-byte pieces:
-// rows of CW floats, 16-byte chunk c of row r at c ^ (r & 15).
+// rows of CW floats, 16-byte chunk c of row r at c ^ r (modulo the row's chunks).
 template <int CW>
 __device__ __forceinline__ void mt_get8(const uint8_t* reg, int r, int col, float (&v)[8]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const f32x4 x = *reinterpret_cast<const f32x4*>(reg + r * (CW * 4) + ((((col >> 2) + h) ^ (r & 15)) << 4));
+        const f32x4 x = *reinterpret_cast<const f32x4*>(reg + r * (CW * 4) + ((((col >> 2) + h) ^ (r & (CW / 4 - 1))) << 4));
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[4 * h + i] = x[i];
     }
@@ -307,16 +314,19 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
 #pragma unroll
         for (int j = 0; j < MI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int wr0 = (w % WR) * (BR / WR), wc0 = (w / WR) * (BC / WC);
-    const int ns = (kdim + MT_K - 1) / MT_K;
+    // stages [sb, ns) of the contraction: all, or this split's share
+    const int nall = (kdim + MT_K - 1) / MT_K;
+    const int each = (nall + a.ksplits - 1) / a.ksplits;
+    const int sb = min(nall, (int)blockIdx.z * each), ns = min(nall, sb + each);
     static_assert(ST == 2 || MODE != MM_WGRAD, "the pair loads are counted in two-stage waits only");
-    if (ns > 0) {
-        load_pairs(0);
+    if (sb < ns) {
+        load_pairs(sb);
 #pragma unroll
         for (int s = 0; s < ST - 1; ++s)
-            if (s < ns) issue(s);
-        load_pairs(1);
+            if (sb + s < ns) issue(sb + s);
+        load_pairs(sb + 1);
     }
-    for (int st = 0; st < ns; ++st) {
+    for (int st = sb; st < ns; ++st) {
         if (ST > 2 && st + ST - 2 < ns)
             mt_wait_vm<(ST - 2) * LPS>();
         else
@@ -327,7 +337,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
             load_pairs(st + ST);
         }
         uint8_t* buf = lds + (st % ST) * STB;
-        if (st == ns - 1 && kdim % MT_K) {
+        if (st == nall - 1 && kdim % MT_K) {
             RowOp::clear_tail(buf, kdim % MT_K, tid);
             ColOp::clear_tail(buf + RowOp::BYTES, kdim % MT_K, tid);
             __syncthreads();
@@ -351,11 +361,14 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
     // accumulators a lane holds columns 4q .. 4q+3 of row m of each 16 x 16
     // block.
     constexpr int CW = BC / WC, WROWS = BR / WR;
-    constexpr int RP = ST * STB / NW / (CW * 4) >= WROWS ? WROWS : ST * STB / NW / (CW * 4) / 16 * 16;
-    static_assert(RP >= 16 && WROWS % RP == 0 && CW == 64, "passes of whole row tiles");
+    constexpr int FIT = ST * STB / NW / (CW * 4);   // rows of the wave's region
+    constexpr int RP = FIT >= WROWS ? WROWS : (FIT >= WROWS / 2 ? WROWS / 2 : WROWS / 4);
+    static_assert(RP >= 16 && RP % 16 == 0 && RP <= FIT && (CW & (CW - 1)) == 0 && CW >= 32, "passes of whole row tiles");
     const uint16_t* bias = nullptr;
     if (MODE == MM_FWD && a.bias) bias = static_cast<const uint16_t*>(a.bias) + (size_t)ch.group * a.N;
     const int rows = MODE == MM_WGRAD ? a.N - r0 : ch.n;
+    const size_t row0 = MODE == MM_WGRAD ? (size_t)ch.group * a.N + r0 : (size_t)ch.row0;   // first output row
+    float* part = a.ksplits > 1 ? a.kpart + (size_t)blockIdx.z * a.kpart_stride : nullptr;
     uint8_t* reg = lds + w * (RP * CW * 4);
     __syncthreads();
 #pragma unroll
@@ -365,68 +378,212 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
         for (int j = 0; j < RP / 16; ++j)
 #pragma unroll
             for (int i = 0; i < NI; ++i)
-                *reinterpret_cast<f32x4*>(reg + (16 * j + m) * (CW * 4) + (((4 * i + q) ^ m) << 4)) =
+                *reinterpret_cast<f32x4*>(reg + (16 * j + m) * (CW * 4) + (((4 * i + q) ^ (m & (CW / 4 - 1))) << 4)) =
                     acc[i][p * (RP / 16) + j];
         const int rbase = wr0 + p * RP;
         if (MODE == MM_FWD && glu) {
             // 16 gate columns, then the 16 up columns they pair with
-            const int c8 = lane & 3, col = 32 * (c8 >> 1) + 8 * (c8 & 1);
+            constexpr int LR = CW / 16;   // lanes per row
+            const int c8 = lane & (LR - 1), col = 32 * (c8 >> 1) + 8 * (c8 & 1);
             const int f = ((c0 + wc0) >> 1) + 8 * c8, cnt = (a.N >> 1) - f;
 #pragma unroll 1
-            for (int rr = lane >> 2; rr < RP; rr += 16) {
+            for (int rr = lane / LR; rr < RP; rr += 64 / LR) {
                 float g[8], u[8];
                 mt_get8<CW>(reg, rr, col, g);
                 mt_get8<CW>(reg, rr, col + 16, u);
-                if (rbase + rr < rows && cnt > 0) mt_out8_glu(a, bias, ch.row0 + rbase + rr, f, cnt, g, u);
+                if (rbase + rr >= rows || cnt <= 0) continue;
+                if (part) {
+                    float* o = part + (row0 + rbase + rr) * a.ldp + f;
+                    mt_st8(o, g, cnt, cnt >= 8);
+                    mt_st8(o + (a.N >> 1), u, cnt, cnt >= 8 && (a.N & 7) == 0);
+                } else {
+                    mt_out8_glu(a, bias, ch.row0 + rbase + rr, f, cnt, g, u);
+                }
             }
         } else {
-            const int col = 8 * (lane & 7), n = c0 + wc0 + col, cnt = (MODE == MM_FWD ? a.N : a.K) - n;
+            constexpr int LR = CW / 8;
+            const int col = 8 * (lane & (LR - 1)), n = c0 + wc0 + col, cnt = (MODE == MM_FWD ? a.N : a.K) - n;
 #pragma unroll 1
-            for (int rr = lane >> 3; rr < RP; rr += 8) {
+            for (int rr = lane / LR; rr < RP; rr += 64 / LR) {
                 float v[8];
                 mt_get8<CW>(reg, rr, col, v);
                 if (rbase + rr >= rows || cnt <= 0) continue;
-                if constexpr (MODE == MM_FWD) {
-                    mt_out8(a, bias, ch.row0 + rbase + rr, n, cnt, v);
-                } else {
-                    G* o = MODE == MM_DGRAD ? static_cast<G*>(a.dx) + (size_t)(ch.row0 + rbase + rr) * a.ldx
-                                            : static_cast<G*>(a.dw) + ((size_t)ch.group * a.N + r0 + rbase + rr) * a.ldw;
-                    mt_st8(o + n, v, cnt, cnt >= 8);
-                }
+                const size_t r = row0 + rbase + rr;
+                if (part)
+                    mt_st8(part + r * a.ldp + n, v, cnt, cnt >= 8);
+                else if constexpr (MODE == MM_FWD)
+                    mt_out8(a, bias, (int)r, n, cnt, v);
+                else if constexpr (MODE == MM_DGRAD)
+                    mt_st8(static_cast<G*>(a.dx) + r * a.ldx + n, v, cnt, cnt >= 8);
+                else
+                    mt_st8(static_cast<G*>(a.dw) + r * a.ldw + n, v, cnt, cnt >= 8);
             }
+        }
+    }
+}
+
+// Joins the splits of a product, in split order, and finishes the rows as the
+// tile kernel would: 256 columns per workgroup, 8 rows at a time, of one chunk
+// (forward, dgrad) or of MR_ROWS rows of dw.
+constexpr int MR_ROWS = 32;
+template <int MODE, typename G>
+__global__ __launch_bounds__(256) void mt_join_kernel(MmArgs a, int bm) {
+    MmChunk ch;
+    size_t row0;
+    int rows;
+    if constexpr (MODE == MM_WGRAD) {
+        ch.group = 0;
+        row0 = (size_t)blockIdx.y * MR_ROWS;
+        rows = (int)min((int64_t)MR_ROWS, (int64_t)a.E * a.N - (int64_t)row0);
+    } else {
+        if (!mm_chunk(a, blockIdx.y, bm, ch)) return;
+        row0 = ch.row0;
+        rows = ch.n;
+    }
+    const bool glu = MODE == MM_FWD && a.act == MM_SWIGLU;
+    const int cols = MODE != MM_FWD ? a.K : (glu ? a.N >> 1 : a.N);
+    const int n = blockIdx.x * 256 + 8 * (threadIdx.x & 31), cnt = cols - n;
+    if (cnt <= 0) return;
+    const uint16_t* bias = nullptr;
+    if (MODE == MM_FWD && a.bias) bias = static_cast<const uint16_t*>(a.bias) + (size_t)ch.group * a.N;
+    auto sum8 = [&](size_t r, int c, bool vec, float (&v)[8]) {
+        const float* p = a.kpart + r * a.ldp + c;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        for (int s = 0; s < a.ksplits; ++s, p += a.kpart_stride) {
+            if (vec) {
+                const f32x4 x = reinterpret_cast<const f32x4*>(p)[0], y = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] += x[i];
+                    v[4 + i] += y[i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < cnt) v[i] += p[i];
+            }
+        }
+    };
+    for (int rr = threadIdx.x >> 5; rr < rows; rr += 8) {
+        const size_t r = row0 + rr;
+        float v[8];
+        sum8(r, n, cnt >= 8, v);
+        if (MODE == MM_FWD && glu) {
+            float u[8];
+            sum8(r, (a.N >> 1) + n, cnt >= 8 && (a.N & 7) == 0, u);
+            mt_out8_glu(a, bias, (int)r, n, cnt, v, u);
+        } else if constexpr (MODE == MM_FWD) {
+            mt_out8(a, bias, (int)r, n, cnt, v);
+        } else if constexpr (MODE == MM_DGRAD) {
+            mt_st8(static_cast<G*>(a.dx) + r * a.ldx + n, v, cnt, cnt >= 8);
+        } else {
+            mt_st8(static_cast<G*>(a.dw) + r * a.ldw + n, v, cnt, cnt >= 8);
         }
     }
 }
 
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
+// Tile shapes: rows and columns, relative rate of a busy CU.
+struct MtShape {
+    int br, bc;
+    double rate;
+};
+constexpr MtShape MT_SHAPES[] = {{256, 256, 1.0}, {128, 256, 0.85}, {128, 128, 0.75}, {64, 64, 0.4}};
+constexpr int MT_NSHAPES = 4;
+
+// Tile shape and contraction splits: the least of an estimate in units of one
+// 64 x 64 x 64 block on one CU.  Workgroups run 256 at a time (one per CU, or
+// two at half the rate each); a workgroup takes about MT_START blocks' time to
+// fill its first stages; splitting adds a launch and the partial sums' traffic.
+MtPick mt_pick_(int mode, int P, int K, int N, int E) {
+    const int live = E < P ? E : P;
+    const int kdim = mode == MM_FWD ? K : (mode == MM_DGRAD ? N : (P + E - 1) / E);
+    const int ns = cdiv(kdim, MT_K);
+    MtPick best{0, 1};
+    double least = 1e300;
+    for (int i = 0; i < MT_NSHAPES; ++i) {
+        const MtShape& t = MT_SHAPES[i];
+        double tiles;
+        if (mode == MM_WGRAD)
+            tiles = (double)cdiv(N, t.br) * cdiv(K, t.bc) * E;
+        else
+            tiles = (E == 1 ? (double)cdiv(P, t.br) : (double)P / t.br + 0.5 * live > live ? (double)P / t.br + 0.5 * live
+                                                                                            : (double)live) *
+                    cdiv(mode == MM_FWD ? N : K, t.bc);
+        const double block = (double)t.br * t.bc / 4096.0 / t.rate;
+        for (int s = 1; s <= MT_MAX_SPLITS && (s == 1 || (i >= 2 && ns / s >= 4 && tiles * s <= 512.0)); s *= 2) {
+            const double rounds = tiles * s <= 256.0 ? 1.0 : tiles * s / 256.0 + 0.5;
+            double cost = rounds * (block * cdiv(ns, s) + MT_START);
+            if (s > 1) cost += MT_JOIN + (double)tiles * s * t.br * t.bc * 4.0 * 2.0 / MT_BYTES;
+            if (cost < least) {
+                least = cost;
+                best = MtPick{i, s};
+            }
+        }
+    }
+    return best;
+}
+
 template <int MODE, int BR, int BC, int WR, int WC, int ST, typename G>
 hipError_t mt_launch(const MmArgs& a, hipStream_t s) {
     const int tr = MODE == MM_WGRAD ? cdiv(a.N, BR) : (a.chunks ? a.max_chunks : cdiv(a.P, BR));
     const int tc = cdiv(MODE == MM_FWD ? a.N : a.K, BC);
     const int64_t total = (int64_t)tr * tc;
-    const dim3 g((uint32_t)((total + 7) / 8 * 8), MODE == MM_WGRAD ? (uint32_t)a.E : 1u);
+    const dim3 g((uint32_t)((total + 7) / 8 * 8), MODE == MM_WGRAD ? (uint32_t)a.E : 1u, (uint32_t)a.ksplits);
     mt_kernel<MODE, BR, BC, WR, WC, ST, G><<<g, 64 * WR * WC, 0, s>>>(a, tr, tc);
+    if (a.ksplits > 1) {
+        const int cols = MODE != MM_FWD ? a.K : (a.act == MM_SWIGLU ? a.N / 2 : a.N);
+        const dim3 j((uint32_t)cdiv(cols, 256),
+                     (uint32_t)(MODE == MM_WGRAD ? cdiv((int64_t)a.E * a.N, MR_ROWS) : tr));
+        mt_join_kernel<MODE, G><<<j, 256, 0, s>>>(a, BR);
+    }
     return hipGetLastError();
+}
+
+template <int MODE, typename G>
+hipError_t mt_run(const MmArgs& a, int shape, hipStream_t s) {
+    constexpr int DEEP = MODE == MM_WGRAD ? 2 : 3;   // (wgrad's pair loads are counted in two-stage waits only)
+    switch (shape) {
+        case 0: return mt_launch<MODE, 256, 256, 2, 4, 2, G>(a, s);
+        case 1: return mt_launch<MODE, 128, 256, 2, 4, DEEP, G>(a, s);
+        case 2: return mt_launch<MODE, 128, 128, 2, 2, 2, G>(a, s);
+        default: return mt_launch<MODE, 64, 64, 2, 2, DEEP, G>(a, s);
+    }
 }
 
 }  // namespace
 
-int mt_chunk_rows(int P, int E) { return P / E <= 160 ? 128 : 256; }
+MtPick mt_pick(int mode, int P, int K, int N, int E) { return mt_pick_(mode, P, K, N, E); }
+int mt_chunk_rows(int mode, int P, int K, int N, int E) { return MT_SHAPES[mt_pick(mode, P, K, N, E).shape].br; }
 
-hipError_t launch_mt_forward(const MmArgs& a, hipStream_t s) {
-    if (mt_chunk_rows(a.P, a.E) == 128) return mt_launch<MM_FWD, 128, 256, 2, 4, 3, uint16_t>(a, s);
-    return mt_launch<MM_FWD, 256, 256, 2, 4, 2, uint16_t>(a, s);
+size_t mt_split_bytes(int mode, int P, int K, int N, int E, bool exact) {
+    // the bound: at most 512 tiles of up to 128 x 128 in all splits together,
+    // and at most MT_MAX_SPLITS splits
+    const int64_t kdim = mode == MM_FWD ? K : (mode == MM_DGRAD ? N : P);
+    if (cdiv(kdim, MT_K) < 8) return 0;
+    const int64_t rows = mode == MM_WGRAD ? (int64_t)E * N : P, cols = mode == MM_FWD ? N : K;
+    const int64_t one = rows * ((cols + 7) / 8 * 8);
+    if (exact) {
+        const int splits = mt_pick(mode, P, K, N, E).splits;
+        return splits > 1 ? (size_t)splits * one * 4 : 0;
+    }
+    const int64_t all = MT_MAX_SPLITS * one;
+    const int64_t cap = (int64_t)512 * 128 * 128;
+    return (size_t)(all < cap ? all : cap) * 4;
 }
 
-hipError_t launch_mt_dgrad(const MmArgs& a, hipStream_t s) {
-    if (mt_chunk_rows(a.P, a.E) == 128) return mt_launch<MM_DGRAD, 128, 256, 2, 4, 3, uint16_t>(a, s);
-    return mt_launch<MM_DGRAD, 256, 256, 2, 4, 2, uint16_t>(a, s);
-}
-
-hipError_t launch_mt_wgrad(const MmArgs& a, hipStream_t s) {
-    if (a.grad_f32) return mt_launch<MM_WGRAD, 256, 256, 2, 4, 2, float>(a, s);
-    return mt_launch<MM_WGRAD, 256, 256, 2, 4, 2, uint16_t>(a, s);
+hipError_t launch_mt(const MmArgs& a0, int mode, hipStream_t s) {
+    MmArgs a = a0;
+    const MtPick pick = mt_pick(mode, a.P, a.K, a.N, a.E);
+    a.ksplits = pick.splits;
+    a.ldp = ((mode == MM_FWD ? a.N : a.K) + 7) / 8 * 8;
+    a.kpart_stride = (size_t)(mode == MM_WGRAD ? (int64_t)a.E * a.N : (int64_t)a.P) * a.ldp;
+    if (mode == MM_FWD) return mt_run<MM_FWD, uint16_t>(a, pick.shape, s);
+    if (mode == MM_DGRAD) return mt_run<MM_DGRAD, uint16_t>(a, pick.shape, s);
+    if (a.grad_f32) return mt_run<MM_WGRAD, float>(a, pick.shape, s);
+    return mt_run<MM_WGRAD, uint16_t>(a, pick.shape, s);
 }
 
 }  // namespace ds4
