@@ -166,7 +166,7 @@ size_t mt_split_bytes(int mode, int P, int K, int N, int E, bool exact);
 hipError_t launch_mt(const MmArgs& a, int mode, hipStream_t s);
 
 // bf16 forward products of few rows (matmul_rows.hip).
-bool mr_takes(int P, int E);
+bool mr_takes(int P, int N, int E);
 hipError_t launch_mr_forward(const MmArgs& a, hipStream_t s);
 
 }  // namespace ds4

@@ -5,12 +5,15 @@
 // rows (SwiGLU: 16 gate rows and the 16 up rows they pair with); its 8 waves
 // share the contraction KW ways (and weight rows 8 / KW ways where the
 // contraction is short), so that a small product still has enough waves to
-// keep the memory busy.  Per step of 128 contraction columns, lane quarter q
-// owns columns 32q .. 32q+31 of its row: 64 contiguous bytes per lane, 256 per
-// weight row; the token operand takes the same columns, so the matrix
-// instruction (v_mfma_f32_16x16x32_bf16, weights first) sees a permuted
-// contraction, which is the same sum.  Two steps are in flight per wave.  The
-// waves' partial sums are joined in LDS in wave order.
+// keep the memory busy.  A step is 128 contraction columns, 4 loads of 64
+// contiguous bytes of each of 16 weight rows, two steps in flight per wave
+// (256 contiguous bytes as 4 pieces 64 bytes apart, each load touching twice
+// the lines, took 136 us for one token's gate/up products instead of 80, and
+// non-temporal loads 98).  Weights go first into the matrix instruction
+// (v_mfma_f32_16x16x32_bf16), so a lane's results belong to one token.  The
+// waves' partial sums are joined in LDS in wave order.  4.3 TB/s on one
+// 7168 x 7168 product (24 us), 5.8 TB/s on one token's gate/up products of 8
+// experts (80 us), 6.3 TB/s on a 131072 x 7168 head (300 us).
 //
 // The rows' group is found from the offsets in the kernel (a plan launch would
 // cost more than the product): workgroup row p of the grid is sorted row p,
@@ -92,16 +95,16 @@ __global__ __launch_bounds__(64 * MR_WAVES) void mr_kernel(MmArgs a, int kw) {
     for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     u32x4 wv[2][RT][4], xv[2][4];
     auto load = [&](int b, int s) {
-        const int c = s * MR_STEP + 32 * q;
+        const int c = s * MR_STEP + 8 * q;
 #pragma unroll
         for (int t = 0; t < RT; ++t)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                wv[b][t][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wr[t] + c) + j);
+                wv[b][t][j] = reinterpret_cast<const u32x4*>(wr[t] + c)[4 * j];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             xv[b][j] = u32x4{0, 0, 0, 0};
-            if (has) xv[b][j] = reinterpret_cast<const u32x4*>(xr + c)[j];
+            if (has) xv[b][j] = reinterpret_cast<const u32x4*>(xr + c)[4 * j];
         }
     };
     auto mma = [&](int b) {
@@ -124,14 +127,14 @@ __global__ __launch_bounds__(64 * MR_WAVES) void mr_kernel(MmArgs a, int kw) {
             }
         }
         if (kpart == kw - 1 && a.K % MR_STEP) {   // the last columns, masked
-            const int c = full * (MR_STEP / 8) + 4 * q;
+            const int c = full * (MR_STEP / 8) + q;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const u32x4 xt = has ? mr_masked(xr, c + j, a.K) : u32x4{0, 0, 0, 0};
+                const u32x4 xt = has ? mr_masked(xr, c + 4 * j, a.K) : u32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
                     acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8, mr_masked(wr[t], c + j, a.K)), __builtin_bit_cast(bf16x8, xt), acc[t],
+                        __builtin_bit_cast(bf16x8, mr_masked(wr[t], c + 4 * j, a.K)), __builtin_bit_cast(bf16x8, xt), acc[t],
                         0, 0, 0);
             }
         }
@@ -171,10 +174,19 @@ int mr_kw(int K) {
 
 }  // namespace
 
-// Rows up to which the products take these kernels (dense; grouped).
-constexpr int MR_MAX_ROWS = 16, MR_MAX_PAIRS = 64;
-
-bool mr_takes(int P, int E) { return P <= (E > 1 ? MR_MAX_PAIRS : MR_MAX_ROWS); }
+// Products that take these kernels, measured against the tile kernels:
+//   dense, 7168 wide: 1 row of 131072 columns 300 us against 320, 8 rows a tie
+//     (323), 16 rows 369 against 320 (the rows' own reads from L2 grow to half
+//     the weights'); with fewer columns also 16 rows win (7168 columns 31.6
+//     against 35.0 us, the tiles being too few).
+//   grouped (256 experts, 4096 columns of 7168): 8 pairs 80 us against 119,
+//     64 pairs 552 against 597, 256 pairs 1527 against 1648, 512 pairs a tie;
+//     with several pairs per expert the tiles win (64 pairs of 16 experts 104
+//     against 95, 128 of 64 experts 504 against 575).
+bool mr_takes(int P, int N, int E) {
+    if (E > 1) return P <= 16 || (P <= 256 && P <= 2 * E);
+    return P <= 8 || (P <= 16 && N < 32768);
+}
 
 hipError_t launch_mr_forward(const MmArgs& a, hipStream_t s) {
     const int kw = mr_kw(a.K), ng = MR_WAVES / kw;

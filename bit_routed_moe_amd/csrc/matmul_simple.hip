@@ -157,12 +157,12 @@ int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 }  // namespace
 
 int mm_chunk_rows(bool f32, int mode, int P, int K, int N, int E) {
-    if (!f32 && mode == MM_FWD && mr_takes(P, E)) return 0;
+    if (!f32 && mode == MM_FWD && mr_takes(P, N, E)) return 0;
     return f32 ? MS_T : mt_chunk_rows(mode, P, K, N, E);
 }
 
 size_t mm_split_bytes(bool f32, int mode, int P, int K, int N, int E, bool exact) {
-    if (f32 || (exact && mode == MM_FWD && mr_takes(P, E))) return 0;
+    if (f32 || (exact && mode == MM_FWD && mr_takes(P, N, E))) return 0;
     return mt_split_bytes(mode, P, K, N, E, exact);
 }
 
@@ -172,7 +172,7 @@ hipError_t launch_mm_forward(const MmArgs& a, bool f32, hipStream_t s) {
     if (f32)
         ms_kernel<float, MM_FWD, float><<<g, 256, 0, s>>>(a, tm, tn);
     else
-        return mr_takes(a.P, a.E) ? launch_mr_forward(a, s) : launch_mt(a, MM_FWD, s);
+        return mr_takes(a.P, a.N, a.E) ? launch_mr_forward(a, s) : launch_mt(a, MM_FWD, s);
     return hipGetLastError();
 }
 

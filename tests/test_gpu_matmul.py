@@ -515,3 +515,40 @@ def test_wrong_device_is_refused():
     with pytest.raises(ds4.Ds4MoeError) as ei:
         ds4.linear(m, 4, x, y, y)
     assert ei.value.status == -1
+
+
+@pytest.mark.parametrize("rows", [1, 8, 9, 16, 17, 33])
+@pytest.mark.parametrize("K", [128, 520, 1031, 2100])
+def test_few_rows(rows, K):
+    """Decoding's sizes: contractions shorter and longer than a workgroup's waves share, with every epilogue."""
+    for N, act in ((40, "none"), (272, "swiglu"), (34, "swiglu"), (1000, "gelu")):
+        p = Problem(rows, K, N, "bf16", act, bias=True, residual=True, seed=rows + K)
+        p.forward()
+        p.check_forward()
+
+
+@pytest.mark.parametrize("mode", ["forward", "dx", "dw"])
+def test_split_contraction(mode):
+    """Few outputs over a long contraction: partial sums of its splits, joined in order, the same every time."""
+    for rows, K, N, groups in ((40, 4104, 72, None), (100, 8192, 130, None), (60, 2056, 264, [30, 0, 25]),
+                               (4100, 72, 40, None), (70, 96, 4104, None), (3000, 40, 136, [1500, 3, 1497])):
+        print(f"split {mode} {rows}x{K}->{N}", flush=True)
+        p = Problem(rows, K, N, "bf16", "swiglu", groups=groups, bias=True, seed=K)
+        if mode == "forward":
+            p.forward()
+            p.check_forward()
+            first = p.y.clone()
+            p.forward()
+            assert torch.equal(first[: p.off_h[-1]], p.y[: p.off_h[-1]])
+        else:
+            want = {w: w == mode for w in ("dx", "dw", "dbias")}
+            p.backward(**want)
+            p.check_backward(**want)
+
+
+def test_wide_head_few_rows():
+    """A head wide enough that 16 rows take the tiles and 3 rows the streaming kernel."""
+    for rows in (3, 16):
+        p = Problem(rows, 264, 33000, "bf16", "none", seed=rows, save=False)
+        p.forward()
+        p.check_forward()
