@@ -154,6 +154,7 @@ __global__ __launch_bounds__(256) void mm_dbias_kernel(const float* __restrict__
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
     float s = 0.0f;
+#pragma unroll 8
     for (int j = 0; j < splits; ++j) s += partial[(size_t)j * n + i];
     mm_st(dbias + i, s);
 }

@@ -10,9 +10,10 @@
 //
 // A workgroup computes BR x BC outputs in stages of 64 contraction columns,
 // which global_load_lds_dwordx4 brings into a ring of LDS buffers without
-// passing through registers.  One barrier per stage: after it the stage has
-// landed for every wave and every wave is done with the one before, whose
-// buffer the next request fills.
+// passing through registers.  Fragments are read one step of 32 columns ahead
+// of the matrix instructions that take them.  One barrier per stage, in its
+// middle: there every wave has read the stage, whose buffer the next request
+// fills, and the stage after it has landed.
 //   Contiguous along k: tile row r is 128 bytes, its 16-byte chunk c in slot
 //     c ^ ((r >> 1) & 7), so a fragment read (16 rows at one chunk per lane
 //     quarter, ds_read_b128) covers all 64 banks.
@@ -30,8 +31,6 @@ namespace {
 
 constexpr int MT_K = 64;            // contraction columns per stage
 constexpr int MT_MAX_SPLITS = 16;   // of the contraction
-// Estimates of mt_pick_, in 64 x 64 x 64 blocks on one CU (about 0.13 us).
-constexpr double MT_START = 20.0, MT_JOIN = 30.0, MT_BYTES = 4e5;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
@@ -214,6 +213,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
     constexpr int STB = RowOp::BYTES + ColOp::BYTES;
     constexpr int MI = BR / WR / 16, NI = BC / WC / 16;
     constexpr int LPS = RowOp::ND + ColOp::ND;   // DMAs per wave and stage
+    constexpr bool PIPE = MODE != MM_WGRAD && BC == 256;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[ST * STB];
     const uint32_t lds32 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -278,34 +278,35 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
             }
         }
     };
-    auto issue = [&](int st) {
+    // DMA i (0 .. LPS-1) of stage st
+    auto issue1 = [&](int st, int i) {
         const uint32_t buf = lds32 + (uint32_t)(st % ST) * STB;
-#pragma unroll
-        for (int i = 0; i < RowOp::ND; ++i) {
+        const uint16_t* p;
+        if (i < RowOp::ND) {
             const int lr = RowOp::lds_row(i, w, lane);
-            const uint16_t* p;
             if constexpr (MODE == MM_WGRAD)
                 p = rsrc[i] + (size_t)min(st * MT_K + lr, kdim - 1) * a.lddz;
             else
                 p = rsrc[i] + 8 * min(st * (MT_K / 8) + RowOp::chunk(lr, lane), kchunk);
             mt_dma16(p, buf + (uint32_t)(i * NW + w) * 1024u);
-        }
-#pragma unroll
-        for (int i = 0; i < ColOp::ND; ++i) {
-            const int lr = ColOp::lds_row(i, w, lane);
-            const uint16_t* p;
+        } else {
+            const int c = i - RowOp::ND, lr = ColOp::lds_row(c, w, lane);
             if constexpr (MODE == MM_FWD) {
-                p = csrc[i] + 8 * min(st * (MT_K / 8) + ColOp::chunk(lr, lane), kchunk);
+                p = csrc[c] + 8 * min(st * (MT_K / 8) + ColOp::chunk(lr, lane), kchunk);
             } else if constexpr (MODE == MM_DGRAD) {
-                p = csrc[i] + (size_t)min(st * MT_K + lr, kdim - 1) * a.ldw;
+                p = csrc[c] + (size_t)min(st * MT_K + lr, kdim - 1) * a.ldw;
             } else {
                 int s = ch.row0 + min(st * MT_K + lr, kdim - 1);
                 if (a.sorted_pair)
-                    s = min((int)((uint32_t)pair[i] / (uint32_t)a.top_k), a.x_rows - 1);
-                p = csrc[i] + (size_t)s * a.ldx;
+                    s = min((int)((uint32_t)pair[c] / (uint32_t)a.top_k), a.x_rows - 1);
+                p = csrc[c] + (size_t)s * a.ldx;
             }
-            mt_dma16(p, buf + RowOp::BYTES + (uint32_t)(i * NW + w) * 1024u);
+            mt_dma16(p, buf + RowOp::BYTES + (uint32_t)(c * NW + w) * 1024u);
         }
+    };
+    auto issue = [&](int st) {
+#pragma unroll
+        for (int i = 0; i < LPS; ++i) issue1(st, i);
     };
 
     f32x4 acc[NI][MI];
@@ -319,41 +320,98 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
     const int each = (nall + a.ksplits - 1) / a.ksplits;
     const int sb = min(nall, (int)blockIdx.z * each), ns = min(nall, sb + each);
     static_assert(ST == 2 || MODE != MM_WGRAD, "the pair loads are counted in two-stage waits only");
-    if (sb < ns) {
-        load_pairs(sb);
-#pragma unroll
-        for (int s = 0; s < ST - 1; ++s)
-            if (sb + s < ns) issue(sb + s);
-        load_pairs(sb + 1);
-    }
-    for (int st = sb; st < ns; ++st) {
-        if (ST > 2 && st + ST - 2 < ns)
-            mt_wait_vm<(ST - 2) * LPS>();
-        else
-            mt_wait_vm<0>();
-        mt_barrier();
-        if (st + ST - 1 < ns) {
-            issue(st + ST - 1);
-            load_pairs(st + ST);
-        }
-        uint8_t* buf = lds + (st % ST) * STB;
+    auto clear_tail = [&](int st) {   // behind the contraction's end, in the last stage
         if (st == nall - 1 && kdim % MT_K) {
-            RowOp::clear_tail(buf, kdim % MT_K, tid);
-            ColOp::clear_tail(buf + RowOp::BYTES, kdim % MT_K, tid);
+            RowOp::clear_tail(lds + (st % ST) * STB, kdim % MT_K, tid);
+            ColOp::clear_tail(lds + (st % ST) * STB + RowOp::BYTES, kdim % MT_K, tid);
             __syncthreads();
         }
+    };
+    // Matrix instructions on fragments rf, cf while the next ones are read
+    // from step ks of stage st (and, with more, stage `more`'s DMAs issued),
+    // spread over the row tiles.
+    auto step = [&](const bf16x8 (&rf)[MI], const bf16x8 (&cf)[NI], bf16x8 (&rn)[MI], bf16x8 (&cn)[NI], int st, int ks,
+                    int more) {
+        const uint8_t* buf = lds + (st % ST) * STB;
 #pragma unroll
-        for (int ks = 0; ks < MT_K / 32; ++ks) {
-            bf16x8 rf[MI], cf[NI];
+        for (int j = 0; j < MI; ++j) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) cf[i] = ColOp::frag(buf + RowOp::BYTES, wc0, i, ks, lane);
+            for (int i = 0; i < NI; ++i)
+                if (i * MI / NI == j) cn[i] = ColOp::frag(buf + RowOp::BYTES, wc0, i, ks, lane);
+            rn[j] = RowOp::frag(buf, wr0, j, ks, lane);
 #pragma unroll
-            for (int j = 0; j < MI; ++j) rf[j] = RowOp::frag(buf, wr0, j, ks, lane);
+            for (int i = 0; i < NI; ++i)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cf[i], rf[j], acc[i][j], 0, 0, 0);
+            if (more >= 0) {
 #pragma unroll
-            for (int j = 0; j < MI; ++j)
+                for (int i = 0; i < LPS; ++i)
+                    if (i * MI / LPS == j) issue1(more, i);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    if constexpr (PIPE) {
+        if (sb < ns) {
 #pragma unroll
-                for (int i = 0; i < NI; ++i)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cf[i], rf[j], acc[i][j], 0, 0, 0);
+            for (int s = 0; s < ST; ++s)
+                if (sb + s < ns) issue(sb + s);
+            if (sb + ST <= ns)
+                mt_wait_vm<(ST - 1) * LPS>();
+            else
+                mt_wait_vm<0>();
+            mt_barrier();
+            clear_tail(sb);
+            bf16x8 rf[2][MI], cf[2][NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) cf[0][i] = ColOp::frag(lds + (sb % ST) * STB + RowOp::BYTES, wc0, i, 0, lane);
+#pragma unroll
+            for (int j = 0; j < MI; ++j) rf[0][j] = RowOp::frag(lds + (sb % ST) * STB, wr0, j, 0, lane);
+            for (int st = sb; st < ns; ++st) {
+                step(rf[0], cf[0], rf[1], cf[1], st, 1, -1);
+                // stage st is read; stage st + 1 has to have landed
+                if (ST > 2 && st + ST - 1 < ns)
+                    mt_wait_vm<(ST - 2) * LPS>();
+                else
+                    mt_wait_vm<0>();
+                mt_barrier();
+                if (st + 1 < ns) clear_tail(st + 1);
+                // (past the last stage the fragments read are not used)
+                step(rf[1], cf[1], rf[0], cf[0], st + 1, 0, st + ST < ns ? st + ST : -1);
+            }
+        }
+    } else {
+        if (sb < ns) {
+            load_pairs(sb);
+#pragma unroll
+            for (int s = 0; s < ST - 1; ++s)
+                if (sb + s < ns) issue(sb + s);
+            load_pairs(sb + 1);
+        }
+        for (int st = sb; st < ns; ++st) {
+            if (ST > 2 && st + ST - 2 < ns)
+                mt_wait_vm<(ST - 2) * LPS>();
+            else
+                mt_wait_vm<0>();
+            mt_barrier();
+            if (st + ST - 1 < ns) {
+                issue(st + ST - 1);
+                load_pairs(st + ST);
+            }
+            clear_tail(st);
+            const uint8_t* buf = lds + (st % ST) * STB;
+#pragma unroll
+            for (int ks = 0; ks < MT_K / 32; ++ks) {
+                bf16x8 rf[MI], cf[NI];
+#pragma unroll
+                for (int i = 0; i < NI; ++i) cf[i] = ColOp::frag(buf + RowOp::BYTES, wc0, i, ks, lane);
+#pragma unroll
+                for (int j = 0; j < MI; ++j) rf[j] = RowOp::frag(buf, wr0, j, ks, lane);
+#pragma unroll
+                for (int j = 0; j < MI; ++j)
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cf[i], rf[j], acc[i][j], 0, 0, 0);
+            }
         }
     }
 
@@ -423,22 +481,21 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
 }
 
 // Joins the splits of a product, in split order, and finishes the rows as the
-// tile kernel would: 256 columns per workgroup, 8 rows at a time, of one chunk
-// (forward, dgrad) or of MR_ROWS rows of dw.
-constexpr int MR_ROWS = 32;
+// tile kernel would: 8 rows of 256 columns per workgroup, rows 8 * blockIdx.z
+// on of one chunk (forward, dgrad), or 8 * blockIdx.y on of dw.
 template <int MODE, typename G>
 __global__ __launch_bounds__(256) void mt_join_kernel(MmArgs a, int bm) {
     MmChunk ch;
-    size_t row0;
-    int rows;
+    size_t r;
     if constexpr (MODE == MM_WGRAD) {
         ch.group = 0;
-        row0 = (size_t)blockIdx.y * MR_ROWS;
-        rows = (int)min((int64_t)MR_ROWS, (int64_t)a.E * a.N - (int64_t)row0);
+        r = (size_t)blockIdx.y * 8 + (threadIdx.x >> 5);
+        if (r >= (size_t)a.E * a.N) return;
     } else {
         if (!mm_chunk(a, blockIdx.y, bm, ch)) return;
-        row0 = ch.row0;
-        rows = ch.n;
+        const int rr = blockIdx.z * 8 + (threadIdx.x >> 5);
+        if (rr >= ch.n) return;
+        r = (size_t)(ch.row0 + rr);
     }
     const bool glu = MODE == MM_FWD && a.act == MM_SWIGLU;
     const int cols = MODE != MM_FWD ? a.K : (glu ? a.N >> 1 : a.N);
@@ -446,57 +503,64 @@ __global__ __launch_bounds__(256) void mt_join_kernel(MmArgs a, int bm) {
     if (cnt <= 0) return;
     const uint16_t* bias = nullptr;
     if (MODE == MM_FWD && a.bias) bias = static_cast<const uint16_t*>(a.bias) + (size_t)ch.group * a.N;
-    auto sum8 = [&](size_t r, int c, bool vec, float (&v)[8]) {
+    auto sum8 = [&](int c, bool vec, float (&v)[8]) {
         const float* p = a.kpart + r * a.ldp + c;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-        for (int s = 0; s < a.ksplits; ++s, p += a.kpart_stride) {
-            if (vec) {
-                const f32x4 x = reinterpret_cast<const f32x4*>(p)[0], y = reinterpret_cast<const f32x4*>(p)[1];
+        if (vec) {
+#pragma unroll 4
+            for (int s = 0; s < a.ksplits; ++s) {
+                const f32x4* x = reinterpret_cast<const f32x4*>(p + s * a.kpart_stride);
+                const f32x4 lo = x[0], hi = x[1];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    v[i] += x[i];
-                    v[4 + i] += y[i];
+                    v[i] += lo[i];
+                    v[4 + i] += hi[i];
                 }
-            } else {
+            }
+        } else {
+            for (int s = 0; s < a.ksplits; ++s)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (i < cnt) v[i] += p[i];
-            }
+                    if (i < cnt) v[i] += p[s * a.kpart_stride + i];
         }
     };
-    for (int rr = threadIdx.x >> 5; rr < rows; rr += 8) {
-        const size_t r = row0 + rr;
-        float v[8];
-        sum8(r, n, cnt >= 8, v);
-        if (MODE == MM_FWD && glu) {
-            float u[8];
-            sum8(r, (a.N >> 1) + n, cnt >= 8 && (a.N & 7) == 0, u);
-            mt_out8_glu(a, bias, (int)r, n, cnt, v, u);
-        } else if constexpr (MODE == MM_FWD) {
-            mt_out8(a, bias, (int)r, n, cnt, v);
-        } else if constexpr (MODE == MM_DGRAD) {
-            mt_st8(static_cast<G*>(a.dx) + r * a.ldx + n, v, cnt, cnt >= 8);
-        } else {
-            mt_st8(static_cast<G*>(a.dw) + r * a.ldw + n, v, cnt, cnt >= 8);
-        }
+    float v[8];
+    sum8(n, cnt >= 8, v);
+    if (MODE == MM_FWD && glu) {
+        float u[8];
+        sum8((a.N >> 1) + n, cnt >= 8 && (a.N & 7) == 0, u);
+        mt_out8_glu(a, bias, (int)r, n, cnt, v, u);
+    } else if constexpr (MODE == MM_FWD) {
+        mt_out8(a, bias, (int)r, n, cnt, v);
+    } else if constexpr (MODE == MM_DGRAD) {
+        mt_st8(static_cast<G*>(a.dx) + r * a.ldx + n, v, cnt, cnt >= 8);
+    } else {
+        mt_st8(static_cast<G*>(a.dw) + r * a.ldw + n, v, cnt, cnt >= 8);
     }
 }
 
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// Tile shapes: rows and columns, relative rate of a busy CU.
+// Tile shapes, with what was measured of them over M = 24 .. 4096 rows of
+// 512 .. 8192 x 512 .. 8192 products, all three modes within 15% (us per stage
+// of 64 contraction columns): lat of a workgroup by itself on its CU, thr per
+// workgroup and CU when the chip is full; wgs that share a CU, so that one's
+// start and end hide behind another's stages.
 struct MtShape {
     int br, bc;
-    double rate;
+    double lat, thr;
+    int wgs;
 };
-constexpr MtShape MT_SHAPES[] = {{256, 256, 1.0}, {128, 256, 0.85}, {128, 128, 0.75}, {64, 64, 0.4}};
+constexpr MtShape MT_SHAPES[] = {
+    {256, 256, 1.1, 1.75, 1}, {128, 256, 0.68, 0.95, 1}, {128, 128, 0.55, 0.5, 2}, {64, 64, 0.25, 0.18, 3}};
 constexpr int MT_NSHAPES = 4;
+constexpr double MT_ENDS = 3.0;    // us to fill a workgroup's first stages and to write its tile
+constexpr double MT_JOIN = 4.0;    // us of a join launch
+constexpr double MT_MEM = 4.0e6;   // bytes per us, of outputs and partial sums
 
-// Tile shape and contraction splits: the least of an estimate in units of one
-// 64 x 64 x 64 block on one CU.  Workgroups run 256 at a time (one per CU, or
-// two at half the rate each); a workgroup takes about MT_START blocks' time to
-// fill its first stages; splitting adds a launch and the partial sums' traffic.
+// Tile shape and contraction splits of the least estimated time: a CU's
+// workgroups times their stages, plus what does not overlap.
 MtPick mt_pick_(int mode, int P, int K, int N, int E) {
     const int live = E < P ? E : P;
     const int kdim = mode == MM_FWD ? K : (mode == MM_DGRAD ? N : (P + E - 1) / E);
@@ -505,20 +569,26 @@ MtPick mt_pick_(int mode, int P, int K, int N, int E) {
     double least = 1e300;
     for (int i = 0; i < MT_NSHAPES; ++i) {
         const MtShape& t = MT_SHAPES[i];
-        double tiles;
+        double tr;   // row tiles; of ragged groups about half a tile each is not filled
         if (mode == MM_WGRAD)
-            tiles = (double)cdiv(N, t.br) * cdiv(K, t.bc) * E;
+            tr = (double)cdiv(N, t.br) * E;
+        else if (E == 1)
+            tr = cdiv(P, t.br);
         else
-            tiles = (E == 1 ? (double)cdiv(P, t.br) : (double)P / t.br + 0.5 * live > live ? (double)P / t.br + 0.5 * live
-                                                                                            : (double)live) *
-                    cdiv(mode == MM_FWD ? N : K, t.bc);
-        const double block = (double)t.br * t.bc / 4096.0 / t.rate;
+            tr = (double)P / t.br + 0.5 * live > live ? (double)P / t.br + 0.5 * live : live;
+        const double tiles = tr * cdiv(mode == MM_FWD ? N : K, t.bc);
+        const double out = tiles * t.br * t.bc * 2.0 / MT_MEM;
         for (int s = 1; s <= MT_MAX_SPLITS && (s == 1 || (i >= 2 && ns / s >= 4 && tiles * s <= 512.0)); s *= 2) {
-            const double rounds = tiles * s <= 256.0 ? 1.0 : tiles * s / 256.0 + 0.5;
-            double cost = rounds * (block * cdiv(ns, s) + MT_START);
-            if (s > 1) cost += MT_JOIN + (double)tiles * s * t.br * t.bc * 4.0 * 2.0 / MT_BYTES;
-            if (cost < least) {
-                least = cost;
+            const double wgs = tiles * s, per_cu = wgs <= 256.0 ? wgs / 256.0 : (double)(int64_t)(wgs / 256.0 + 0.999);
+            const double stage = t.thr * per_cu > t.lat ? t.thr * per_cu : t.lat;
+            double us = stage * cdiv(ns, s);
+            if (t.wgs == 1)
+                us += MT_ENDS * (per_cu < 1.0 ? 1.0 : per_cu) + out;
+            else
+                us = (us > out ? us : out) + MT_ENDS;
+            if (s > 1) us += MT_JOIN + (double)wgs * t.br * t.bc * 8.0 / MT_MEM;
+            if (us < least) {
+                least = us;
                 best = MtPick{i, s};
             }
         }
@@ -536,7 +606,7 @@ hipError_t mt_launch(const MmArgs& a, hipStream_t s) {
     if (a.ksplits > 1) {
         const int cols = MODE != MM_FWD ? a.K : (a.act == MM_SWIGLU ? a.N / 2 : a.N);
         const dim3 j((uint32_t)cdiv(cols, 256),
-                     (uint32_t)(MODE == MM_WGRAD ? cdiv((int64_t)a.E * a.N, MR_ROWS) : tr));
+                     (uint32_t)(MODE == MM_WGRAD ? cdiv((int64_t)a.E * a.N, 8) : tr), MODE == MM_WGRAD ? 1u : BR / 8u);
         mt_join_kernel<MODE, G><<<j, 256, 0, s>>>(a, BR);
     }
     return hipGetLastError();
