@@ -31,6 +31,7 @@ namespace {
 
 constexpr int MT_K = 64;            // contraction columns per stage
 constexpr int MT_MAX_SPLITS = 16;   // of the contraction
+constexpr int MT_RING = 2048;       // wgrad: row numbers kept in LDS
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
@@ -247,7 +248,6 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
     // fixed part of each DMA's source address
     const uint16_t* rsrc[RowOp::ND];
     const uint16_t* csrc[ColOp::ND];
-    int pair[ColOp::ND];   // wgrad: x rows of the next stage (sorted_pair entries)
 #pragma unroll
     for (int i = 0; i < RowOp::ND; ++i) {
         const int lr = RowOp::lds_row(i, w, lane);
@@ -269,13 +269,14 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
         }
     }
     const int kchunk = (kdim - 1) / 8;
-    auto load_pairs = [&](int st) {
-        if constexpr (MODE == MM_WGRAD) {
-            if (a.sorted_pair) {
-#pragma unroll
-                for (int i = 0; i < ColOp::ND; ++i)
-                    pair[i] = a.sorted_pair[ch.row0 + min(st * MT_K + ColOp::lds_row(i, w, lane), kdim - 1)];
-            }
+    // wgrad's x rows: a ring of 32 stages' row numbers in LDS, 16 stages filled
+    // at a time (pair ids loaded a stage ahead into registers put their latency
+    // into every stage's wait: 3.4 us a stage, 1.7 without them)
+    __shared__ int src_rows[MODE == MM_WGRAD ? MT_RING : 1];
+    auto fill_rows = [&](int st) {
+        if (MODE == MM_WGRAD && a.sorted_pair) {
+            for (int i = st * MT_K + tid; i < (st + MT_RING / MT_K / 2) * MT_K && i < kdim; i += NW * 64)
+                src_rows[i % MT_RING] = mm_src(a, ch.row0 + i);
         }
     };
     // DMA i (0 .. LPS-1) of stage st
@@ -296,10 +297,8 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
             } else if constexpr (MODE == MM_DGRAD) {
                 p = csrc[c] + (size_t)min(st * MT_K + lr, kdim - 1) * a.ldw;
             } else {
-                int s = ch.row0 + min(st * MT_K + lr, kdim - 1);
-                if (a.sorted_pair)
-                    s = min((int)((uint32_t)pair[c] / (uint32_t)a.top_k), a.x_rows - 1);
-                p = csrc[c] + (size_t)s * a.ldx;
+                const int i = min(st * MT_K + lr, kdim - 1);
+                p = csrc[c] + (size_t)(a.sorted_pair ? src_rows[i % MT_RING] : ch.row0 + i) * a.ldx;
             }
             mt_dma16(p, buf + RowOp::BYTES + (uint32_t)(c * NW + w) * 1024u);
         }
@@ -319,7 +318,6 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
     const int nall = (kdim + MT_K - 1) / MT_K;
     const int each = (nall + a.ksplits - 1) / a.ksplits;
     const int sb = min(nall, (int)blockIdx.z * each), ns = min(nall, sb + each);
-    static_assert(ST == 2 || MODE != MM_WGRAD, "the pair loads are counted in two-stage waits only");
     auto clear_tail = [&](int st) {   // behind the contraction's end, in the last stage
         if (st == nall - 1 && kdim % MT_K) {
             RowOp::clear_tail(lds + (st % ST) * STB, kdim % MT_K, tid);
@@ -380,12 +378,16 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
             }
         }
     } else {
+        constexpr int HALF = MT_RING / MT_K / 2;   // stages per filling
         if (sb < ns) {
-            load_pairs(sb);
+            if (MODE == MM_WGRAD && a.sorted_pair) {
+                fill_rows(sb / HALF * HALF);
+                fill_rows(sb / HALF * HALF + HALF);
+                __syncthreads();
+            }
 #pragma unroll
             for (int s = 0; s < ST - 1; ++s)
                 if (sb + s < ns) issue(sb + s);
-            load_pairs(sb + 1);
         }
         for (int st = sb; st < ns; ++st) {
             if (ST > 2 && st + ST - 2 < ns)
@@ -393,10 +395,9 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
             else
                 mt_wait_vm<0>();
             mt_barrier();
-            if (st + ST - 1 < ns) {
-                issue(st + ST - 1);
-                load_pairs(st + ST);
-            }
+            if (st + ST - 1 < ns) issue(st + ST - 1);
+            // (the half behind stage st has been read; it is needed again in 8 stages)
+            if (st % HALF == HALF / 2 && st / HALF > sb / HALF) fill_rows((st / HALF + 1) * HALF);
             clear_tail(st);
             const uint8_t* buf = lds + (st % ST) * STB;
 #pragma unroll
@@ -553,11 +554,13 @@ struct MtShape {
     int wgs;
 };
 constexpr MtShape MT_SHAPES[] = {
-    {256, 256, 1.1, 1.75, 1}, {128, 256, 0.68, 0.95, 1}, {128, 128, 0.55, 0.5, 2}, {64, 64, 0.25, 0.18, 3}};
+    {256, 256, 1.1, 1.6, 1}, {128, 256, 0.68, 0.95, 1}, {128, 128, 0.55, 0.5, 2}, {64, 64, 0.25, 0.18, 3}};
 constexpr int MT_NSHAPES = 4;
 constexpr double MT_ENDS = 3.0;    // us to fill a workgroup's first stages and to write its tile
+constexpr double MT_WENDS = 0.9;   // the same of wgrad's, without the writing
 constexpr double MT_JOIN = 4.0;    // us of a join launch
-constexpr double MT_MEM = 4.0e6;   // bytes per us, of outputs and partial sums
+constexpr double MT_MEM = 4.5e6;   // bytes per us, of outputs and partial sums
+constexpr double MT_RAGGED = 1.25; // small tiles of groups read their weights more often
 
 // Tile shape and contraction splits of the least estimated time: a CU's
 // workgroups times their stages, plus what does not overlap.
@@ -580,9 +583,12 @@ MtPick mt_pick_(int mode, int P, int K, int N, int E) {
         const double out = tiles * t.br * t.bc * 2.0 / MT_MEM;
         for (int s = 1; s <= MT_MAX_SPLITS && (s == 1 || (i >= 2 && ns / s >= 4 && tiles * s <= 512.0)); s *= 2) {
             const double wgs = tiles * s, per_cu = wgs <= 256.0 ? wgs / 256.0 : (double)(int64_t)(wgs / 256.0 + 0.999);
-            const double stage = t.thr * per_cu > t.lat ? t.thr * per_cu : t.lat;
+            const double thr = t.thr * (t.wgs > 1 && E > 1 && mode != MM_WGRAD ? MT_RAGGED : 1.0);
+            const double stage = thr * per_cu > t.lat ? thr * per_cu : t.lat;
             double us = stage * cdiv(ns, s);
-            if (t.wgs == 1)
+            if (mode == MM_WGRAD)   // (few stages: the writing does not hide)
+                us += MT_WENDS * (per_cu < 1.0 ? 1.0 : per_cu) + out;
+            else if (t.wgs == 1)
                 us += MT_ENDS * (per_cu < 1.0 ? 1.0 : per_cu) + out;
             else
                 us = (us > out ? us : out) + MT_ENDS;
@@ -614,7 +620,7 @@ hipError_t mt_launch(const MmArgs& a, hipStream_t s) {
 
 template <int MODE, typename G>
 hipError_t mt_run(const MmArgs& a, int shape, hipStream_t s) {
-    constexpr int DEEP = MODE == MM_WGRAD ? 2 : 3;   // (wgrad's pair loads are counted in two-stage waits only)
+    constexpr int DEEP = 3;
     switch (shape) {
         case 0: return mt_launch<MODE, 256, 256, 2, 4, 2, G>(a, s);
         case 1: return mt_launch<MODE, 128, 256, 2, 4, DEEP, G>(a, s);
