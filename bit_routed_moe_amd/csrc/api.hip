@@ -347,11 +347,11 @@ int check_mm(const ds4moe_matmul* m, int32_t rows) {
 
 int64_t mm_quantum(const ds4moe_matmul* m) { return m->dtype == DS4MOE_DT_F32 ? 4 : 8; }
 
-// Row splits of the bias gradient: about 64 rows each when the groups are
-// even, at most 64 splits.
+// Row splits of the element-wise pass and the bias gradient: about 32 rows
+// each when the groups are even, at most 128 splits.
 int mm_splits(const ds4moe_matmul* m, int32_t rows) {
-    const int64_t s = ((int64_t)rows + 64 * (int64_t)m->groups - 1) / (64 * (int64_t)m->groups);
-    return (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
+    const int64_t s = ((int64_t)rows + 32 * (int64_t)m->groups - 1) / (32 * (int64_t)m->groups);
+    return (int)(s < 1 ? 1 : (s > 128 ? 128 : s));
 }
 
 int mm_max_chunks(const ds4moe_matmul* m, int32_t rows, int bm) {

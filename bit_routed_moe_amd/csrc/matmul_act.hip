@@ -94,10 +94,11 @@ __global__ __launch_bounds__(256) void mm_dz_kernel(MmArgs a, T* __restrict__ dz
     const int len = (n + a.splits - 1) / a.splits;
     const int b = min(n, (int)blockIdx.y * len), e = min(n, b + len);
     const bool vec = nc == 8, vecu = vec && (a.N & 15) == 0;   // (up columns start at N/2)
-    const T* dy = static_cast<const T*>(a.dy);
-    const T* zp = static_cast<const T*>(a.zin);
+    const T* __restrict__ dy = static_cast<const T*>(a.dy);
+    const T* __restrict__ zp = static_cast<const T*>(a.zin);
     float sum[NP][8] = {};
     if (nc > 0) {
+#pragma unroll 2
         for (int i = b + lr; i < e; i += DZ_ROWS) {
             const size_t r = (size_t)(row0 + i);
             float g[8], d[NP][8];

@@ -554,7 +554,7 @@ struct MtShape {
     int wgs;
 };
 constexpr MtShape MT_SHAPES[] = {
-    {256, 256, 1.1, 1.6, 1}, {128, 256, 0.68, 0.95, 1}, {128, 128, 0.55, 0.5, 2}, {64, 64, 0.25, 0.18, 3}};
+    {256, 256, 1.1, 1.6, 1}, {128, 256, 0.68, 0.95, 1}, {128, 128, 0.55, 0.55, 2}, {64, 64, 0.25, 0.18, 3}};
 constexpr int MT_NSHAPES = 4;
 constexpr double MT_ENDS = 3.0;    // us to fill a workgroup's first stages and to write its tile
 constexpr double MT_WENDS = 0.9;   // the same of wgrad's, without the writing
