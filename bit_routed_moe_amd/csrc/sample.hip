@@ -120,16 +120,26 @@ struct SpRow {
             }
 #pragma unroll
             for (int j = 0; j < UN; ++j) {
-                const int c = c0 + j * NT;
+                const int c = c0 + j * NT, i0 = c * N - skip;
+                if (c >= ce || i0 < 0 || i0 + N > V) {   // what is not the row's becomes -infinity
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        if (c < ce && i0 + i >= 0 && i0 + i < V) continue;
+                        if constexpr (sizeof(T) == 4)
+                            v[j][i] = 0xFF800000u;
+                        else
+                            v[j][i >> 1] = (i & 1) ? (v[j][i >> 1] & 0xFFFFu) | 0xFF800000u
+                                                   : (v[j][i >> 1] & 0xFFFF0000u) | 0xFF80u;
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const int idx = c * N + i - skip;
                     float l;
                     if constexpr (sizeof(T) == 4)
                         l = __uint_as_float(v[j][i]);
                     else
                         l = __uint_as_float((i & 1) ? v[j][i >> 1] & 0xFFFF0000u : v[j][i >> 1] << 16);
-                    if (c < ce && idx >= 0 && idx < V && l > -INFINITY) f(l, idx);
+                    if (l > -INFINITY) f(l, i0 + i);
                 }
             }
         }
@@ -394,18 +404,22 @@ __global__ __launch_bounds__(SP_THREADS) void sp_hist_kernel(SpArgs a) {
         table[i] = sp_bin_exp(i);
     }
     __syncthreads();
+    // only top-k asks for counts
+    const bool counts = a.top_k && a.top_k[r] > 0;
     row.template each<SP_THREADS>(sp, a.S, [&](float l, int) {
         const double d = row.dist(l);
         const int b = row.bin(d);
-        if (b < SP_BINS) sp_count(cnt, mass, b, sp_weight(d, table[b]));
+        if (b < SP_BINS) {
+            if (counts) atomicAdd(cnt + b, 1u);
+            atomicAdd(reinterpret_cast<unsigned long long*>(mass + b), (unsigned long long)sp_weight(d, table[b]));
+        }
     });
     __syncthreads();
     for (int i = threadIdx.x; i < SP_BINS; i += SP_THREADS) {
-        if (cnt[i]) {
-            atomicAdd(a.cnt + (size_t)r * SP_BINS + i, cnt[i]);
+        if (cnt[i]) atomicAdd(a.cnt + (size_t)r * SP_BINS + i, cnt[i]);
+        if (mass[i])
             atomicAdd(reinterpret_cast<unsigned long long*>(a.mass + (size_t)r * SP_BINS + i),
                       (unsigned long long)mass[i]);
-        }
     }
 }
 
@@ -593,7 +607,7 @@ __device__ SpHit sp_narrow(SpShared& s, const SpRow<T>& row, bool by_rank, uint6
     const int b = by_rank ? sp_find(s.C, t) : sp_find(s.M, t);
     uint32_t c0 = b ? s.C[b - 1] : 0;
     uint64_t m0 = b ? s.M[b - 1] : 0;
-    uint32_t n = s.C[b] - c0;
+    uint32_t n = SP_CAP + 1;   // (rows without top-k are not counted)
     uint32_t lo = 0, hi = 0xFFFFFFFFu;
     while (n > SP_CAP && lo < hi) {   // (each round divides the range by 2048)
         int shift = 0;
