@@ -850,7 +850,7 @@ int ds4moe_grouped_matmul_backward(const ds4moe_matmul* m, int32_t rows, const v
 }
 
 size_t ds4moe_sample_workspace_bytes(int32_t B, int32_t V) {
-    if (B < 1 || B > 65536 || V < 1 || V > (1 << 20)) return 0;
+    if (B < 1 || B > 32768 || V < 1 || V > (1 << 20)) return 0;
     return ds4::sample_workspace_bytes(B, V);
 }
 
@@ -861,7 +861,7 @@ int ds4moe_sample(int32_t B, int32_t V, const void* logits, int64_t ld, int32_t 
         if (dtype == DS4MOE_DT_FP8_E4M3) return fail(DS4MOE_E_UNSUPPORTED, "fp8 logits");
         return fail(DS4MOE_E_ARG, "dtype %d", dtype);
     }
-    if (B < 1 || B > 65536) return fail(DS4MOE_E_SHAPE, "B %d not in [1, 65536]", B);
+    if (B < 1 || B > 32768) return fail(DS4MOE_E_SHAPE, "B %d not in [1, 32768]", B);
     if (V < 1 || V > (1 << 20)) return fail(DS4MOE_E_SHAPE, "V %d not in [1, 2^20]", V);
     if (ld < V || ld > ((int64_t)1 << 31)) return fail(DS4MOE_E_SHAPE, "ld %lld for rows of %d", (long long)ld, V);
     REQ_PTR(logits);

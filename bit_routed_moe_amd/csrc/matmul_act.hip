@@ -24,14 +24,33 @@ __global__ __launch_bounds__(1024) void mm_plan_kernel(const int32_t* __restrict
     const int nch = (n + bm - 1) / bm;
     int total;
     const int base = block_exclusive_scan(nch, tmp, &total);
-    for (int i = 0; i < nch && base + i < cmax; ++i) {   // (overlapping ranges of corrupt offsets stop at cmax)
+    // chunk i of the group (overlapping ranges of corrupt offsets stop at cmax)
+    auto put = [&](int group, int at, int first, int rows, int i) {
+        if (at + i >= cmax) return;
         MmChunk c;
-        c.group = e;
-        c.row0 = row0 + i * bm;
-        c.n = min(bm, n - i * bm);
+        c.group = group;
+        c.row0 = first + i * bm;
+        c.n = min(bm, rows - i * bm);
         c.pad = 0;
-        chunks[base + i] = c;
+        chunks[at + i] = c;
+    };
+    // groups of many chunks are written by all threads
+    __shared__ int many, place[4][1024];
+    if (e == 0) many = 0;
+    __syncthreads();
+    if (nch <= 8) {
+        for (int i = 0; i < nch; ++i) put(e, base, row0, n, i);
+    } else {
+        const int k = atomicAdd(&many, 1);
+        place[0][k] = e;
+        place[1][k] = base;
+        place[2][k] = row0;
+        place[3][k] = n;
     }
+    __syncthreads();
+    for (int k = 0; k < many; ++k)
+        for (int i = e; i < (place[3][k] + bm - 1) / bm; i += 1024)
+            put(place[0][k], place[1][k], place[2][k], place[3][k], i);
     if (e == 0) n_chunks[0] = min(total, cmax);
 }
 

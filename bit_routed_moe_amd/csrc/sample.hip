@@ -468,11 +468,11 @@ struct SpShared {
     int at;
 };
 
-// Sorts the s.n collected keys descending: a bitonic network over SP_KEYS keys
-// per thread in registers (key h of a thread is element tid + h * SP_LAST),
-// exchanged by lane shuffles (distances below 64), LDS (below SP_LAST) or
-// within the thread.
-__device__ __forceinline__ void sp_sort(SpShared& s) {
+// Sorts more than SP_LAST collected keys descending: a bitonic network over
+// SP_KEYS keys per thread in registers (key h of a thread is element
+// tid + h * SP_LAST), exchanged by lane shuffles (distances below 64), LDS
+// (below SP_LAST) or within the thread.
+__device__ __forceinline__ void sp_sort_network(SpShared& s) {
     const int tid = threadIdx.x, n = (int)s.n;
     int size = 64;
     while (size < n) size <<= 1;
@@ -495,26 +495,64 @@ __device__ __forceinline__ void sp_sort(SpShared& s) {
                 }
             }
         }
-        for (int j = min(k >> 1, SP_LAST / 2); j >= 1; j >>= 1) {
-            if (j >= WAVE) {
+        for (int j = min(k >> 1, SP_LAST / 2); j >= WAVE; j >>= 1) {
 #pragma unroll
-                for (int h = 0; h < SP_KEYS; ++h)
-                    if (tid + h * SP_LAST < size) s.key[tid + h * SP_LAST] = v[h];
-                __syncthreads();
-            }
+            for (int h = 0; h < SP_KEYS; ++h)
+                if (tid + h * SP_LAST < size) s.key[tid + h * SP_LAST] = v[h];
+            __syncthreads();
 #pragma unroll
             for (int h = 0; h < SP_KEYS; ++h) {
                 const int i = tid + h * SP_LAST;
                 if ((i & ~63) >= size) continue;   // (whole waves past the end)
-                const uint64_t o = j >= WAVE ? s.key[i ^ j] : (uint64_t)__shfl_xor(v[h], j, WAVE);
+                const uint64_t o = s.key[i ^ j];
                 const bool want_max = ((i & k) == 0) == ((i & j) == 0);
                 v[h] = want_max ? (v[h] > o ? v[h] : o) : (v[h] < o ? v[h] : o);
             }
-            if (j >= WAVE) __syncthreads();
+            __syncthreads();
+        }
+#pragma unroll
+        for (int j = WAVE / 2; j >= 1; j >>= 1) {
+            if (j >= k) continue;
+#pragma unroll
+            for (int h = 0; h < SP_KEYS; ++h) {
+                const int i = tid + h * SP_LAST;
+                if ((i & ~63) >= size) continue;
+                const uint64_t o = (uint64_t)__shfl_xor(v[h], j, WAVE);
+                const bool want_max = ((i & k) == 0) == ((i & j) == 0);
+                v[h] = want_max ? (v[h] > o ? v[h] : o) : (v[h] < o ? v[h] : o);
+            }
         }
     }
 #pragma unroll
     for (int h = 0; h < SP_KEYS; ++h) s.key[tid + h * SP_LAST] = v[h];
+    __syncthreads();
+}
+
+// Sorts the s.n collected keys descending.  Up to one per thread: a key's
+// place is the number of greater ones, counted by as many threads per key as
+// there are (109 keys 14,200 cycles with the network, whose 28 steps are one
+// LDS round trip each).
+__device__ __forceinline__ void sp_sort(SpShared& s) {
+    const int tid = threadIdx.x, n = (int)s.n;
+    if (n > SP_LAST) {
+        sp_sort_network(s);
+        return;
+    }
+    const int nr = max(WAVE, (n + WAVE - 1) & ~(WAVE - 1));   // (whole waves share a part of the comparisons)
+    const int parts = SP_LAST / nr, part = tid / nr, i = tid - part * nr;
+    if (tid < n) s.rank[tid] = 0;
+    __syncthreads();
+    uint64_t k = 0;
+    if (part < parts && i < n) {
+        k = s.key[i];
+        const int each = (n + parts - 1) / parts, jb = part * each, je = min(n, jb + each);
+        uint32_t greater = 0;
+#pragma unroll 8
+        for (int j = jb; j < je; ++j) greater += s.key[j] > k;
+        if (greater) atomicAdd(&s.rank[i], greater);
+    }
+    __syncthreads();
+    if (part == 0 && i < n) s.key[s.rank[i]] = k;
     __syncthreads();
 }
 
@@ -808,9 +846,11 @@ __global__ __launch_bounds__(SP_LAST) void sp_final_kernel(SpArgs a, bool whole)
 // Rows of at most this many tokens take one launch.
 constexpr int SP_WHOLE = 4096;
 
-// Workgroups per row: 4096 tokens each, but about 1024 in all.
+// Workgroups per row: 4096 tokens each, but about 512 in all (64 rows of 131072
+// 58.7 us, 256 of 50003 80.0; with 1024 61.7 and 83.5, with 2048 77.6 and 96.5:
+// each has the row's histogram to scan).
 int sp_splits(int B, int V) {
-    const int by_len = (V + 4095) / 4096, by_rows = 1024 / B;
+    const int by_len = (V + 4095) / 4096, by_rows = 512 / B;
     const int s = by_len < by_rows ? by_len : by_rows;
     return s < 1 ? 1 : (s > SP_MAX_SPLITS ? SP_MAX_SPLITS : s);
 }

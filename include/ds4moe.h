@@ -414,7 +414,7 @@ size_t ds4moe_matmul_workspace_bytes(const ds4moe_matmul* m, int32_t rows, int32
  * row's last 16-byte piece of memory must belong to the allocation), fp32 or
  * bf16.  temperature, top_p, min_p fp32 [B] and top_k int32 [B] may each be
  * NULL (temperature 1, filter off); u fp32 [B]; token int32 [B]; prob fp32 [B]
- * or NULL.  1 <= B <= 65536, 1 <= V <= 2^20.  workspace: device scratch of
+ * or NULL.  1 <= B <= 32768, 1 <= V <= 2^20.  workspace: device scratch of
  * ds4moe_sample_workspace_bytes(B, V) bytes (NULL if that is 0). */
 int ds4moe_sample(int32_t B, int32_t V, const void* logits, int64_t ld, int32_t dtype, const float* temperature,
                   const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* token,

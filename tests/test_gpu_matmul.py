@@ -552,3 +552,48 @@ def test_wide_head_few_rows():
         p = Problem(rows, 264, 33000, "bf16", "none", seed=rows, save=False)
         p.forward()
         p.check_forward()
+
+
+def test_one_group_of_many_chunks():
+    """A group's rows beyond what one thread of the plan lists by itself."""
+    p = Problem(5003, 72, 40, "bf16", "relu", groups=[2, 4990, 0, 7], gather_k=2, bias=True, seed=5)
+    p.forward()
+    p.check_forward()
+    p.backward()
+    p.check_backward()
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with their own outputs and workspaces."""
+    ps = [Problem(260, 264, 200, "bf16", "swiglu", groups=[130, 0, 130], gather_k=2, bias=True, seed=s) for s in (1, 2)]
+    refs = []
+    for p in ps:
+        p.forward()
+        p.backward()
+        refs.append([t.clone() for t in (p.y, p.z, p.dx, p.dw, p.dbias)])
+    ws = [(p.ws(False), p.ws(True)) for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p, s, (wf, wb) in zip(ps, streams, ws):
+            with torch.cuda.stream(s):
+                p.forward(ws=wf)
+                p.backward(ws=wb)
+    torch.cuda.synchronize()
+    for p, r in zip(ps, refs):
+        for a, b in zip((p.y, p.z, p.dx, p.dw, p.dbias), r):
+            assert torch.equal(a, b)
+
+
+def test_offsets_that_start_behind_zero_and_one_group():
+    """One group of part of the rows: the others are left as they were."""
+    for dtype in ("bf16", "f32"):
+        for rows, a, b in ((12, 3, 9), (300, 17, 290)):
+            p = Problem(rows, 72, 40, dtype, "silu", groups=[rows], bias=True, seed=rows)
+            p.off.copy_(torch.tensor([a, b], dtype=torch.int32))
+            p.off_h = [a, b]
+            p.forward()
+            p.check_forward()
+            p.backward()
+            p.check_backward()
+            assert torch.isnan(p.y[:a].float()).all() and torch.isnan(p.dx[:a].float()).all()

@@ -12,7 +12,7 @@ def call(B=2, V=100, logits=FAKE, ld=100, dtype=0, t=None, k=None, p=None, q=Non
 
 
 def test_refusals():
-    assert call(B=0) == -2 and call(B=65537) == -2 and call(B=-1) == -2
+    assert call(B=0) == -2 and call(B=32769) == -2 and call(B=-1) == -2
     assert call(V=0) == -2 and call(V=(1 << 20) + 1, ld=1 << 21) == -2
     assert call(ld=99) == -2 and call(ld=-100) == -2 and call(ld=(1 << 31) + 1) == -2
     assert call(dtype=2) == -4 and call(dtype=3) == -1 and call(dtype=-1) == -1
