@@ -7,7 +7,7 @@
 // of three masses, and the sampled token is the one at which the running sum
 // first exceeds u times that mass.  The vocabulary is never sorted: each
 // question is "where does a running count or sum cross a value", answered by a
-// histogram over (max - l) / T (64 bins per unit) and then among the tokens of
+// histogram over (max - l) / T (64 bins per unit or more) and then among the tokens of
 // the few bins that the crossings can lie in, which are collected and sorted.
 //
 // Weights are held as integers, round(w * 2^43) in 64 bits, from 64-bit
@@ -29,8 +29,8 @@ namespace ds4 {
 
 namespace {
 
-constexpr int SP_BINS = 2048;                // bin b: b <= 64 (max - l) / T < b + 1
-constexpr double SP_PER_UNIT = 64.0;
+constexpr int SP_BINS = 2048;                // bin b: b <= per (max - l) / T < b + 1
+constexpr double SP_REACH = 31.0;            // (max - l) / T from which a token has no weight
 constexpr int SP_CAP = 2048;                 // tokens sorted at once
 constexpr double SP_ONE = 8796093022208.0;   // 2^43
 constexpr uint64_t SP_ONE_I = (uint64_t)1 << 43;
@@ -48,26 +48,26 @@ struct SpArgs {
     int32_t* token;
     float* prob;
     // workspace, per row
-    uint64_t* best;    // [S] largest route_key of each split
+    uint64_t* best;    // [SP_MAX_SPLITS] largest route_key of each split
+    uint32_t* low;     // [SP_MAX_SPLITS] lowest logit (order-preserving bits)
     uint64_t* mass;    // [SP_BINS]
     uint32_t* cnt;     // [SP_BINS]
     uint64_t* list;    // [SP_CAP] collected keys
     uint32_t* n;       // [64] (first: tokens collected)
 };
 
-// Weight of a token t = 64 (max - l) / T bins below the largest, in bin b:
-// e^(-(b + 1/2)/64) (table or exp) times the series of e^(g/64) for the rest
-// g = b + 1/2 - t, |g| <= 1/2; the first omitted term is below 2^-51.  The
-// rounding to an integer is that of adding 2^52.
-__device__ __forceinline__ double sp_bin_exp(int b) { return SP_ONE * exp(-((double)b + 0.5) * (1.0 / SP_PER_UNIT)); }
-__device__ __forceinline__ uint64_t sp_weight(double t, double ebin) {
-    constexpr double C1 = 1.0 / SP_PER_UNIT, C2 = C1 * C1 / 2, C3 = C2 * C1 / 3, C4 = C3 * C1 / 4, C5 = C4 * C1 / 5;
-    const double g = 0.5 - __builtin_amdgcn_fract(t);
-    double s = fma(g, C5, C4);
-    s = fma(g, s, C3);
-    s = fma(g, s, C2);
-    s = fma(g, s, C1);
-    s = fma(g, s, 1.0);
+// Weight of a token t = per (max - l) / T bins below the largest, in bin b:
+// e^(-(b + 1/2)/per) (table or exp) times the series of e^x for the rest
+// x = (b + 1/2 - t)/per, |x| <= 1/128; the first omitted term is below 2^-51.
+// The rounding to an integer is that of adding 2^52.
+__device__ __forceinline__ double sp_bin_exp(int b, double unit) { return SP_ONE * exp(-((double)b + 0.5) * unit); }
+__device__ __forceinline__ uint64_t sp_weight(double t, double ebin, double unit) {
+    const double x = (0.5 - __builtin_amdgcn_fract(t)) * unit;
+    double s = fma(x, 1.0 / 120.0, 1.0 / 24.0);
+    s = fma(x, s, 1.0 / 6.0);
+    s = fma(x, s, 0.5);
+    s = fma(x, s, 1.0);
+    s = fma(x, s, 1.0);
     return (uint64_t)(__double_as_longlong(fma(ebin, s, 4503599627370496.0)) & 0xFFFFFFFFFFFFFll);
 }
 
@@ -80,18 +80,21 @@ struct SpRow {
     const T* row;
     int V;
     float mx;
-    double scale;   // 64 / T
+    double per;     // bins per unit of (max - l) / T, a power of two
+    double unit;    // 1 / per
+    double scale;   // per / T
+    double limit;   // bins of tokens with weight
 
-    // 64 (max - l) / T; 0 for the largest logits themselves, also infinite ones
+    // per (max - l) / T; 0 for the largest logits themselves, also infinite ones
     __device__ __forceinline__ double dist(float l) const {
         return l == mx ? 0.0 : ((double)mx - (double)l) * scale;
     }
     // Bin of a distance, SP_BINS for tokens of no weight
-    static __device__ __forceinline__ int bin(double t) { return t < 31.0 * SP_PER_UNIT ? (int)t : SP_BINS; }
+    __device__ __forceinline__ int bin(double t) const { return t < limit ? (int)t : SP_BINS; }
     __device__ __forceinline__ uint64_t weight(float l) const {
         const double t = dist(l);
         const int b = bin(t);
-        return b < SP_BINS ? sp_weight(t, sp_bin_exp(b)) : 0;
+        return b < SP_BINS ? sp_weight(t, sp_bin_exp(b, unit), unit) : 0;
     }
 
     // f(logit, index) for the tokens of split s of n that are above -infinity
@@ -152,18 +155,28 @@ __device__ __forceinline__ SpRow<T> sp_row(const SpArgs& a, int r) {
     row.row = static_cast<const T*>(a.logits) + (size_t)r * a.ld;
     row.V = a.V;
     row.mx = 0.0f;
-    row.scale = 1.0;
+    row.per = row.unit = row.scale = row.limit = 1.0;
     return row;
 }
 
-// The row's reference from its largest key; false when nothing is left to
-// choose or the choice is greedy.
+// The row's reference from its largest key and its lowest logit above
+// -infinity (as order-preserving bits); false when nothing is left to choose
+// or the choice is greedy.  64 bins per unit reach all weights; a row of narrow
+// range takes finer bins, 2, 4, ... times as many per unit while all of it
+// still fits, so that few tokens share one.
 template <typename T>
-__device__ __forceinline__ bool sp_reference(const SpArgs& a, int r, uint64_t best, SpRow<T>& row) {
+__device__ __forceinline__ bool sp_reference(const SpArgs& a, int r, uint64_t best, uint32_t low, SpRow<T>& row) {
     const float temp = a.temperature ? a.temperature[r] : 1.0f;
     if (best == 0 || !(temp > 0.0f)) return false;
     row.mx = key_value(best);
-    row.scale = SP_PER_UNIT / (double)temp;
+    const double inv_t = 1.0 / (double)temp;
+    const double range = ((double)row.mx - (double)key_value((uint64_t)low << 32)) * inv_t;
+    row.per = 64.0;
+    if (range < SP_REACH)
+        while (row.per < 16384.0 && range * row.per * 2.0 < SP_BINS - 1) row.per *= 2.0;
+    row.unit = 1.0 / row.per;
+    row.scale = row.per * inv_t;
+    row.limit = SP_REACH * row.per < SP_BINS ? SP_REACH * row.per : (double)SP_BINS;
     return true;
 }
 
@@ -176,25 +189,46 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
     return v;
 }
 
-// The row's largest key from its splits' (at most 64: one per lane).
-constexpr int SP_MAX_SPLITS = 64;
-__device__ __forceinline__ uint64_t sp_row_best(const SpArgs& a, int r) {
-    const int lane = threadIdx.x & 63;
-    return wave_max_u64(lane < a.S ? a.best[(size_t)r * a.S + lane] : 0);
+__device__ __forceinline__ uint32_t wave_min_u32(uint32_t v) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v = min(v, (uint32_t)__shfl_xor((int)v, o, WAVE));
+    return v;
 }
 
-// Largest key of split sp of n (every thread receives it); tmp: NT / 64 words.
+// The row's largest key and lowest logit from its splits' (at most 64: one per
+// lane).
+constexpr int SP_MAX_SPLITS = 64;
+__device__ __forceinline__ uint64_t sp_row_best(const SpArgs& a, int r, uint32_t& low) {
+    const int lane = threadIdx.x & 63;
+    const bool has = lane < a.S;
+    const size_t at = (size_t)r * SP_MAX_SPLITS + lane;
+    low = wave_min_u32(has ? a.low[at] : 0xFFFFFFFFu);
+    return wave_max_u64(has ? a.best[at] : 0);
+}
+
+// The same of split sp of n (every thread receives them); tmp, tmpl: NT / 64
+// words.
 template <int NT, typename T>
-__device__ __forceinline__ uint64_t sp_largest(const SpRow<T>& row, int sp, int n, uint64_t* tmp) {
+__device__ __forceinline__ uint64_t sp_largest(const SpRow<T>& row, int sp, int n, uint64_t* tmp, uint32_t* tmpl,
+                                               uint32_t& low) {
     uint64_t best = 0;
+    float lo = INFINITY;
     row.template each<NT>(sp, n, [&](float l, int idx) {
         const uint64_t k = route_key(l, idx);
         best = best > k ? best : k;
+        lo = fminf(lo, l);
     });
     best = wave_max_u64(best);
-    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = best;
+    low = wave_min_u32(sp_k32(lo));
+    if ((threadIdx.x & 63) == 0) {
+        tmp[threadIdx.x >> 6] = best;
+        tmpl[threadIdx.x >> 6] = low;
+    }
     __syncthreads();
-    for (int i = 0; i < NT / WAVE; ++i) best = best > tmp[i] ? best : tmp[i];
+    for (int i = 0; i < NT / WAVE; ++i) {
+        best = best > tmp[i] ? best : tmp[i];
+        low = min(low, tmpl[i]);
+    }
     __syncthreads();
     return best;
 }
@@ -300,8 +334,8 @@ __device__ __forceinline__ uint64_t sp_target(float u, uint64_t mass) {
 }
 // Smallest weight that min-p keeps, and the bins it can lie in (q <= 1).
 __device__ __forceinline__ uint64_t sp_min_weight(float q) { return (uint64_t)ceil((double)q * SP_ONE); }
-__device__ __forceinline__ void sp_min_bins(float q, int& lo, int& hi) {
-    const int b = (int)(fmin(-log((double)q), 31.0) * SP_PER_UNIT);
+__device__ __forceinline__ void sp_min_bins(float q, double per, int& lo, int& hi) {
+    const int b = (int)fmin(-log((double)q) * per, (double)(SP_BINS - 1));
     lo = max(b - 1, 0);
     hi = min(b + 1, SP_BINS - 1);
 }
@@ -333,7 +367,7 @@ struct SpBins {
                (b >= lo[3] && b <= hi[3]);
     }
 };
-__device__ __forceinline__ SpBins sp_bins(const SpFilters& f, const uint32_t* C, const uint64_t* M) {
+__device__ __forceinline__ SpBins sp_bins(const SpFilters& f, double per, const uint32_t* C, const uint64_t* M) {
     SpBins s;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -362,7 +396,7 @@ __device__ __forceinline__ SpBins sp_bins(const SpFilters& f, const uint32_t* C,
     if (f.q > 1.0f) {
         least = most = SP_ONE_I;
     } else if (f.q > 0.0f) {
-        sp_min_bins(f.q, s.lo[2], s.hi[2]);
+        sp_min_bins(f.q, per, s.lo[2], s.hi[2]);
         uint64_t m = s.lo[2] ? M[s.lo[2] - 1] : 0;
         m = m > SP_ONE_I ? m : SP_ONE_I;
         least = least < m ? least : m;
@@ -373,15 +407,36 @@ __device__ __forceinline__ SpBins sp_bins(const SpFilters& f, const uint32_t* C,
     return s;
 }
 
+// A split's tokens into a histogram in LDS (counts for top-k only).
+template <int NT, typename T>
+__device__ __forceinline__ void sp_histogram(const SpArgs& a, int r, const SpRow<T>& row, int sp, int n, uint32_t* cnt,
+                                             uint64_t* mass, const double* table) {
+    const bool counts = a.top_k && a.top_k[r] > 0;
+    row.template each<NT>(sp, n, [&](float l, int) {
+        const double d = row.dist(l);
+        const int b = row.bin(d);
+        if (b < SP_BINS) {
+            if (counts) atomicAdd(cnt + b, 1u);
+            atomicAdd(reinterpret_cast<unsigned long long*>(mass + b), (unsigned long long)sp_weight(d, table[b], row.unit));
+        }
+    });
+    __syncthreads();
+}
+
 // ---- launches that split a row -----------------------------------------------
 
 template <typename T>
 __global__ __launch_bounds__(SP_THREADS) void sp_max_kernel(SpArgs a) {
     __shared__ uint64_t tmp[SP_THREADS / WAVE];
+    __shared__ uint32_t tmpl[SP_THREADS / WAVE];
     const int sp = blockIdx.x, r = blockIdx.y;
     const SpRow<T> row = sp_row<T>(a, r);
-    const uint64_t best = sp_largest<SP_THREADS>(row, sp, a.S, tmp);
-    if (threadIdx.x == 0) a.best[(size_t)r * a.S + sp] = best;
+    uint32_t low;
+    const uint64_t best = sp_largest<SP_THREADS>(row, sp, a.S, tmp, tmpl, low);
+    if (threadIdx.x == 0) {
+        a.best[(size_t)r * SP_MAX_SPLITS + sp] = best;
+        a.low[(size_t)r * SP_MAX_SPLITS + sp] = low;
+    }
     // the row's histogram and list start empty
     for (int i = sp * SP_THREADS + threadIdx.x; i < SP_BINS; i += a.S * SP_THREADS) {
         a.cnt[(size_t)r * SP_BINS + i] = 0;
@@ -397,24 +452,16 @@ __global__ __launch_bounds__(SP_THREADS) void sp_hist_kernel(SpArgs a) {
     __shared__ double table[SP_BINS];
     const int sp = blockIdx.x, r = blockIdx.y;
     SpRow<T> row = sp_row<T>(a, r);
-    if (!sp_reference(a, r, sp_row_best(a, r), row)) return;
+    uint32_t low;
+    const uint64_t best = sp_row_best(a, r, low);
+    if (!sp_reference(a, r, best, low, row)) return;
     for (int i = threadIdx.x; i < SP_BINS; i += SP_THREADS) {
         cnt[i] = 0;
         mass[i] = 0;
-        table[i] = sp_bin_exp(i);
+        table[i] = sp_bin_exp(i, row.unit);
     }
     __syncthreads();
-    // only top-k asks for counts
-    const bool counts = a.top_k && a.top_k[r] > 0;
-    row.template each<SP_THREADS>(sp, a.S, [&](float l, int) {
-        const double d = row.dist(l);
-        const int b = row.bin(d);
-        if (b < SP_BINS) {
-            if (counts) atomicAdd(cnt + b, 1u);
-            atomicAdd(reinterpret_cast<unsigned long long*>(mass + b), (unsigned long long)sp_weight(d, table[b]));
-        }
-    });
-    __syncthreads();
+    sp_histogram<SP_THREADS>(a, r, row, sp, a.S, cnt, mass, table);
     for (int i = threadIdx.x; i < SP_BINS; i += SP_THREADS) {
         if (cnt[i]) atomicAdd(a.cnt + (size_t)r * SP_BINS + i, cnt[i]);
         if (mass[i])
@@ -433,10 +480,12 @@ __global__ __launch_bounds__(SP_THREADS) void sp_collect_kernel(SpArgs a) {
     __shared__ uint32_t n, at;
     const int sp = blockIdx.x, r = blockIdx.y;
     SpRow<T> row = sp_row<T>(a, r);
-    if (!sp_reference(a, r, sp_row_best(a, r), row)) return;
+    uint32_t low;
+    const uint64_t best = sp_row_best(a, r, low);
+    if (!sp_reference(a, r, best, low, row)) return;
     if (threadIdx.x == 0) n = 0;
     sp_running<SP_THREADS>(a.cnt + (size_t)r * SP_BINS, a.mass + (size_t)r * SP_BINS, C, M, redc, red);
-    const SpBins bins = sp_bins(sp_filters(a, r, C[SP_BINS - 1]), C, M);
+    const SpBins bins = sp_bins(sp_filters(a, r, C[SP_BINS - 1]), row.per, C, M);
     row.template each<SP_THREADS>(sp, a.S, [&](float l, int idx) {
         const int b = row.bin(row.dist(l));
         if (b < SP_BINS && bins.has(b)) {
@@ -719,7 +768,7 @@ template <typename T>
 __device__ __forceinline__ uint64_t sp_mass_from(SpShared& s, const SpRow<T>& row, float q) {
     const uint64_t wq = sp_min_weight(q);
     int lo, hi;
-    sp_min_bins(q, lo, hi);
+    sp_min_bins(q, row.per, lo, hi);
     uint64_t part = 0;
     row.template each<SP_LAST>(0, 1, [&](float l, int) {
         const int b = row.bin(row.dist(l));
@@ -764,8 +813,9 @@ __global__ __launch_bounds__(SP_LAST) void sp_final_kernel(SpArgs a, bool whole)
     __shared__ SpShared s;
     const int tid = threadIdx.x, r = blockIdx.x;
     SpRow<T> row = sp_row<T>(a, r);
-    const uint64_t best = whole ? sp_largest<SP_LAST>(row, 0, 1, s.red) : sp_row_best(a, r);
-    if (!sp_reference(a, r, best, row)) {
+    uint32_t low;
+    const uint64_t best = whole ? sp_largest<SP_LAST>(row, 0, 1, s.red, s.redc, low) : sp_row_best(a, r, low);
+    if (!sp_reference(a, r, best, low, row)) {
         if (tid == 0) {
             a.token[r] = best == 0 ? -1 : sp_key_index(best);
             if (a.prob) a.prob[r] = best == 0 ? 0.0f : 1.0f;
@@ -775,17 +825,15 @@ __global__ __launch_bounds__(SP_LAST) void sp_final_kernel(SpArgs a, bool whole)
     const uint32_t* cnt = s.scnt;
     const uint64_t* mass = s.smass;
     if (whole) {
+        static_assert(SP_CAP >= SP_BINS, "the table fits");
+        double* table = reinterpret_cast<double*>(s.sum);
         for (int i = tid; i < SP_BINS; i += SP_LAST) {
             s.scnt[i] = 0;
             s.smass[i] = 0;
+            table[i] = sp_bin_exp(i, row.unit);
         }
         __syncthreads();
-        row.template each<SP_LAST>(0, 1, [&](float l, int) {
-            const double d = row.dist(l);
-            const int b = row.bin(d);
-            if (b < SP_BINS) sp_count(s.scnt, s.smass, b, sp_weight(d, sp_bin_exp(b)));
-        });
-        __syncthreads();
+        sp_histogram<SP_LAST>(a, r, row, 0, 1, s.scnt, s.smass, table);
     } else {
         cnt = a.cnt + (size_t)r * SP_BINS;
         mass = a.mass + (size_t)r * SP_BINS;
@@ -793,7 +841,7 @@ __global__ __launch_bounds__(SP_LAST) void sp_final_kernel(SpArgs a, bool whole)
     sp_running<SP_LAST>(cnt, mass, s.C, s.M, s.redc, s.red);
     const SpFilters f = sp_filters(a, r, s.C[SP_BINS - 1]);
     if (whole) {
-        const SpBins bins = sp_bins(f, s.C, s.M);
+        const SpBins bins = sp_bins(f, row.per, s.C, s.M);
         sp_gather(s, row, [&](int b, uint32_t) { return bins.has(b); });
     } else {
         if (tid == 0) s.n = a.n[(size_t)r * 64];
@@ -823,7 +871,7 @@ __global__ __launch_bounds__(SP_LAST) void sp_final_kernel(SpArgs a, bool whole)
                 kept = SP_ONE_I;
             } else if (f.q > 0.0f) {
                 int lo, hi;
-                sp_min_bins(f.q, lo, hi);
+                sp_min_bins(f.q, row.per, lo, hi);
                 uint64_t m;
                 if (fits)
                     m = sp_mass_from_sorted(s, f.q, lo ? s.M[lo - 1] : 0);
@@ -843,8 +891,10 @@ __global__ __launch_bounds__(SP_LAST) void sp_final_kernel(SpArgs a, bool whole)
     }
 }
 
-// Rows of at most this many tokens take one launch.
-constexpr int SP_WHOLE = 4096;
+// Rows of at most this many tokens take one launch (8192 tokens: 1 row 22.8 us
+// against 29.8 with four launches, 256 rows 24.4 against 41.3; 32000 tokens: 1
+// row 43 against 30, 64 rows 46 against 41, 512 rows 103 against 101).
+constexpr int SP_WHOLE = 16384;
 
 // Workgroups per row: 4096 tokens each, but about 512 in all (64 rows of 131072
 // 58.7 us, 256 of 50003 80.0; with 1024 61.7 and 83.5, with 2048 77.6 and 96.5:
@@ -875,7 +925,7 @@ size_t sp_align(size_t v) { return (v + 255) & ~(size_t)255; }
 size_t sample_workspace_bytes(int B, int V) {
     if (V <= SP_WHOLE) return 0;
     const size_t b = (size_t)B;
-    return sp_align(b * SP_MAX_SPLITS * 8) + b * (SP_BINS * 8 + SP_BINS * 4 + SP_CAP * 8 + 256);
+    return sp_align(b * SP_MAX_SPLITS * 8) + b * (SP_BINS * 8 + SP_BINS * 4 + SP_CAP * 8 + SP_MAX_SPLITS * 4 + 256);
 }
 
 hipError_t launch_sample(int B, int V, int64_t ld, bool f32, const void* logits, const float* temperature,
@@ -904,6 +954,8 @@ hipError_t launch_sample(int B, int V, int64_t ld, bool f32, const void* logits,
     a.cnt = reinterpret_cast<uint32_t*>(ws);
     ws += b * SP_BINS * 4;
     a.n = reinterpret_cast<uint32_t*>(ws);
+    ws += b * 256;
+    a.low = reinterpret_cast<uint32_t*>(ws);
     return f32 ? sp_launch<float>(a, B, s) : sp_launch<uint16_t>(a, B, s);
 }
 

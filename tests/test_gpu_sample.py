@@ -242,3 +242,16 @@ def test_graph_replays():
         gr.replay()
         torch.cuda.synchronize()
         assert torch.equal(token, refs[rep % 3][0]) and torch.equal(prob, refs[rep % 3][1]), rep
+
+
+def test_crowded_bin_beside_an_outlier():
+    """A far low logit keeps the bins wide, so that nearly all tokens share one and its range is narrowed."""
+    l = normal(5, 60000, 0.004, 15)
+    l[:, 777] = -50.0
+    check(l, seed=1)
+    check(l, p=0.6, seed=2)
+    check(l, k=30001, seed=3)
+    check(l, T=2.0, k=50000, p=0.97, q=0.9951, seed=4)
+    short = l[:, :9000].contiguous()
+    check(short, k=5001, p=0.8, seed=5)
+    check(short.to(torch.bfloat16), p=0.7, seed=6)
