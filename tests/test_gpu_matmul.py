@@ -597,3 +597,38 @@ def test_offsets_that_start_behind_zero_and_one_group():
             p.backward()
             p.check_backward()
             assert torch.isnan(p.y[:a].float()).all() and torch.isnan(p.dx[:a].float()).all()
+
+
+# sizes that between them take every tile shape in every direction (and split contractions), with ragged ends
+@pytest.mark.parametrize("rows,K,N", [(2045, 2050, 7170), (4090, 7162, 2042), (1021, 1026, 7170), (700, 1026, 5000)])
+def test_large_linear_shapes(rows, K, N):
+    print(f"large {rows}x{K}->{N}", flush=True)
+    p = Problem(rows, K, N, "bf16", "swiglu", bias=True, residual=True, seed=rows)
+    p.forward()
+    p.check_forward()
+    p.backward()
+    p.check_backward()
+    del p
+    p = Problem(rows, K, N, "bf16", "gelu", grad="f32", save=False, seed=rows + 1)
+    p.forward()
+    p.check_forward()
+    p.backward(dbias=False)
+    p.check_backward(dbias=False)
+
+
+@pytest.mark.parametrize("groups", [[2600, 0, 1, 3000, 900, 1100, 30, 369], [1] * 3 + [0, 700, 150, 260, 5] * 3 + [90] * 7 +
+                                    [0, 10, 1], [200] * 7 + [100]], ids=["few", "many", "even"])
+def test_large_grouped_shapes(groups):
+    rows = sum(groups) + 11
+    print(f"large grouped {len(groups)} groups, {rows} rows", flush=True)
+    p = Problem(rows, 1026, 2042, "bf16", "silu", groups=groups, gather_k=3, bias=True, seed=rows)
+    p.forward()
+    p.check_forward()
+    p.backward()
+    p.check_backward()
+    del p
+    p = Problem(rows, 1026, 2042, "bf16", "none", groups=groups, grad="f32", save=False, seed=rows)
+    p.forward()
+    p.check_forward()
+    p.backward()
+    p.check_backward()
