@@ -214,7 +214,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
     constexpr int STB = RowOp::BYTES + ColOp::BYTES;
     constexpr int MI = BR / WR / 16, NI = BC / WC / 16;
     constexpr int LPS = RowOp::ND + ColOp::ND;   // DMAs per wave and stage
-    constexpr bool PIPE = MODE != MM_WGRAD && BC == 256;
+    constexpr bool PIPE = BC == 256;   // fragments a step ahead (smaller tiles' workgroups cover each other's waits)
     __shared__ __attribute__((aligned(1024))) uint8_t lds[ST * STB];
     const uint32_t lds32 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -245,28 +245,34 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
     const uint16_t* dz = static_cast<const uint16_t*>(a.dz);
     const uint16_t* wg = static_cast<const uint16_t*>(a.w) + (size_t)ch.group * a.N * a.ldw;
 
-    // fixed part of each DMA's source address
-    const uint16_t* rsrc[RowOp::ND];
-    const uint16_t* csrc[ColOp::ND];
+    // fixed parts of the DMAs' source addresses.  The chunk that a lane brings
+    // is the same in all of a wave's DMAs (their rows differ by a multiple of
+    // 16, or of 8 times an even number of waves), so operands contiguous along
+    // the tile need one pointer, the others one per row
+    static_assert(NW % 2 == 0 && (NW * RowOp::RPD) % 16 == 0 && (NW * ColOp::RPD) % 16 == 0, "one chunk per lane");
+    const int rrow = RowOp::lds_row(0, w, lane), crow = ColOp::lds_row(0, w, lane);
+    constexpr int RSTEP = NW * RowOp::RPD, CSTEP = NW * ColOp::RPD;   // rows from DMA to DMA
+    const int rchunk = RowOp::chunk(rrow, lane), cchunk = ColOp::chunk(crow, lane);
+    constexpr int NR = MODE == MM_WGRAD ? 1 : RowOp::ND, NC = MODE == MM_FWD ? ColOp::ND : 1;
+    const uint16_t* rsrc[NR];
+    const uint16_t* csrc[NC];
+    if constexpr (MODE == MM_WGRAD) {
+        rsrc[0] = dz + (size_t)ch.row0 * a.lddz + 8 * min(r0 / 8 + rchunk, (a.N - 1) / 8);
+    } else {
 #pragma unroll
-    for (int i = 0; i < RowOp::ND; ++i) {
-        const int lr = RowOp::lds_row(i, w, lane);
-        if constexpr (MODE == MM_FWD)
-            rsrc[i] = x + (size_t)mm_src(a, ch.row0 + min(lr, ch.n - 1)) * a.ldx;
-        else if constexpr (MODE == MM_DGRAD)
-            rsrc[i] = dz + (size_t)(ch.row0 + min(lr, ch.n - 1)) * a.lddz;
-        else
-            rsrc[i] = dz + (size_t)ch.row0 * a.lddz + 8 * min(r0 / 8 + RowOp::chunk(lr, lane), (a.N - 1) / 8);
-    }
-#pragma unroll
-    for (int i = 0; i < ColOp::ND; ++i) {
-        const int lr = ColOp::lds_row(i, w, lane);
-        if constexpr (MODE == MM_FWD) {
-            const int n = mm_col(a, glu, c0, lr);
-            csrc[i] = wg + (size_t)(n < 0 ? a.N - 1 : n) * a.ldw;
-        } else {
-            csrc[i] = (MODE == MM_DGRAD ? wg : x) + 8 * min(c0 / 8 + ColOp::chunk(lr, lane), (a.K - 1) / 8);
+        for (int i = 0; i < RowOp::ND; ++i) {
+            const int r = ch.row0 + min(rrow + i * RSTEP, ch.n - 1);
+            rsrc[i] = MODE == MM_FWD ? x + (size_t)mm_src(a, r) * a.ldx : dz + (size_t)r * a.lddz;
         }
+    }
+    if constexpr (MODE == MM_FWD) {
+#pragma unroll
+        for (int i = 0; i < ColOp::ND; ++i) {
+            const int n = mm_col(a, glu, c0, crow + i * CSTEP);
+            csrc[i] = wg + (size_t)(n < 0 ? a.N - 1 : n) * a.ldw;
+        }
+    } else {
+        csrc[0] = (MODE == MM_DGRAD ? wg : x) + 8 * min(c0 / 8 + cchunk, (a.K - 1) / 8);
     }
     const int kchunk = (kdim - 1) / 8;
     // wgrad's x rows: a ring of 32 stages' row numbers in LDS, 16 stages filled
@@ -284,21 +290,21 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
         const uint32_t buf = lds32 + (uint32_t)(st % ST) * STB;
         const uint16_t* p;
         if (i < RowOp::ND) {
-            const int lr = RowOp::lds_row(i, w, lane);
             if constexpr (MODE == MM_WGRAD)
-                p = rsrc[i] + (size_t)min(st * MT_K + lr, kdim - 1) * a.lddz;
+                p = rsrc[0] + (size_t)min(st * MT_K + rrow + i * RSTEP, kdim - 1) * a.lddz;
             else
-                p = rsrc[i] + 8 * min(st * (MT_K / 8) + RowOp::chunk(lr, lane), kchunk);
+                p = rsrc[i] + 8 * min(st * (MT_K / 8) + rchunk, kchunk);
             mt_dma16(p, buf + (uint32_t)(i * NW + w) * 1024u);
         } else {
-            const int c = i - RowOp::ND, lr = ColOp::lds_row(c, w, lane);
+            const int c = i - RowOp::ND;
             if constexpr (MODE == MM_FWD) {
-                p = csrc[c] + 8 * min(st * (MT_K / 8) + ColOp::chunk(lr, lane), kchunk);
-            } else if constexpr (MODE == MM_DGRAD) {
-                p = csrc[c] + (size_t)min(st * MT_K + lr, kdim - 1) * a.ldw;
+                p = csrc[c] + 8 * min(st * (MT_K / 8) + cchunk, kchunk);
             } else {
-                const int i = min(st * MT_K + lr, kdim - 1);
-                p = csrc[c] + (size_t)(a.sorted_pair ? src_rows[i % MT_RING] : ch.row0 + i) * a.ldx;
+                const int k = min(st * MT_K + crow + c * CSTEP, kdim - 1);
+                if constexpr (MODE == MM_DGRAD)
+                    p = csrc[0] + (size_t)k * a.ldw;
+                else
+                    p = csrc[0] + (size_t)(a.sorted_pair ? src_rows[k % MT_RING] : ch.row0 + k) * a.ldx;
             }
             mt_dma16(p, buf + RowOp::BYTES + (uint32_t)(c * NW + w) * 1024u);
         }
@@ -348,6 +354,17 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+    constexpr int HALF = MT_RING / MT_K / 2;   // stages per filling of the ring
+    if (MODE == MM_WGRAD && a.sorted_pair && sb < ns) {
+        fill_rows(sb / HALF * HALF);
+        fill_rows(sb / HALF * HALF + HALF);
+        __syncthreads();
+    }
+    // in stage st, behind its barrier: the half of the ring behind stage st has
+    // been read, and is needed again in 6 stages at the earliest
+    auto refill = [&](int st) {
+        if (MODE == MM_WGRAD && st % HALF == HALF / 2 && st / HALF > sb / HALF) fill_rows((st / HALF + 1) * HALF);
+    };
     if constexpr (PIPE) {
         if (sb < ns) {
 #pragma unroll
@@ -373,18 +390,13 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
                     mt_wait_vm<0>();
                 mt_barrier();
                 if (st + 1 < ns) clear_tail(st + 1);
+                refill(st);
                 // (past the last stage the fragments read are not used)
                 step(rf[1], cf[1], rf[0], cf[0], st + 1, 0, st + ST < ns ? st + ST : -1);
             }
         }
     } else {
-        constexpr int HALF = MT_RING / MT_K / 2;   // stages per filling
         if (sb < ns) {
-            if (MODE == MM_WGRAD && a.sorted_pair) {
-                fill_rows(sb / HALF * HALF);
-                fill_rows(sb / HALF * HALF + HALF);
-                __syncthreads();
-            }
 #pragma unroll
             for (int s = 0; s < ST - 1; ++s)
                 if (sb + s < ns) issue(sb + s);
@@ -396,8 +408,7 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
                 mt_wait_vm<0>();
             mt_barrier();
             if (st + ST - 1 < ns) issue(st + ST - 1);
-            // (the half behind stage st has been read; it is needed again in 8 stages)
-            if (st % HALF == HALF / 2 && st / HALF > sb / HALF) fill_rows((st / HALF + 1) * HALF);
+            refill(st);
             clear_tail(st);
             const uint8_t* buf = lds + (st % ST) * STB;
 #pragma unroll
