@@ -348,9 +348,14 @@ int check_mm(const ds4moe_matmul* m, int32_t rows) {
 int64_t mm_quantum(const ds4moe_matmul* m) { return m->dtype == DS4MOE_DT_F32 ? 4 : 8; }
 
 // Row splits of the element-wise pass and the bias gradient: about 32 rows
-// each when the groups are even, at most 128 splits.
+// each when the groups are even (8 rows while 256 columns times that make less
+// than a workgroup per CU), at most 128 splits.
 int mm_splits(const ds4moe_matmul* m, int32_t rows) {
-    const int64_t s = ((int64_t)rows + 32 * (int64_t)m->groups - 1) / (32 * (int64_t)m->groups);
+    const int64_t blocks = ((int64_t)m->out_dim + 255) / 256 * m->groups;
+    auto by = [&](int64_t per) { return ((int64_t)rows + per * m->groups - 1) / (per * m->groups); };
+    int64_t s = by(32);
+    const int64_t fill = (256 + blocks - 1) / blocks, most = by(8);
+    if (s < fill) s = fill < most ? fill : most;
     return (int)(s < 1 ? 1 : (s > 128 ? 128 : s));
 }
 

@@ -1,10 +1,13 @@
 // fp32 products at original precision on the fp32 matrix instructions
 // (v_mfma_f32_16x16x4_f32), every mode in one kernel: 64 x 64 outputs per
 // workgroup of 4 waves, stages of 32 contraction columns through two LDS
-// buffers, the next stage's loads in flight (in registers) while one is
-// worked on.  Tile rows of 36 floats: the 4-column fragment reads and the
-// 16-byte writes then spread over the banks.  Sizes are those of parity runs
-// and of small models; a stage's latency bounds the small ones.
+// buffers, the loads of the two stages after it in flight (in registers) while
+// one is worked on.  In LDS an operand lies as it comes: contiguous along the
+// contraction, rows of 32 + 4 floats and fragments of 4 columns at once;
+// contiguous along the tile, contraction rows of 64 + 4 floats and fragments
+// element by element (written transposed, 16 lanes met in one bank).  Sizes
+// are those of parity runs and of small models; a stage's latency bounds the
+// small ones.
 #include "matmul.hpp"
 
 namespace ds4 {
@@ -13,24 +16,14 @@ namespace {
 
 constexpr int MS_T = 64;       // tile rows and columns
 constexpr int MS_K = 32;       // contraction columns per stage
-constexpr int MS_LD = MS_K + 4;
-
-// Four consecutive elements of a row from element c on; zeros past n.
-__device__ __forceinline__ f32x4 ms_ld4(const float* row, int c, int n) {
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (c + 4 <= n) {
-        v = *reinterpret_cast<const f32x4*>(row + c);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (c + i < n) v[i] = row[c + i];
-    }
-    return v;
-}
+constexpr int MS_LD = MS_K + 4;    // floats per LDS row, contraction along the row
+constexpr int MS_LT = MS_T + 4;    // the same, tile along the row
+constexpr int MS_BUF = MS_T * MS_LD > MS_K * MS_LT ? MS_T * MS_LD : MS_K * MS_LT;
 
 template <int MODE>
 __global__ __launch_bounds__(256) void ms_kernel(MmArgs a, int tiles_m) {
-    __shared__ float As[2][MS_T][MS_LD], Bs[2][MS_T][MS_LD];
+    __shared__ __attribute__((aligned(16))) float As[2][MS_BUF], Bs[2][MS_BUF];
+    constexpr bool AT = MODE == MM_WGRAD, BT = MODE != MM_FWD;   // contiguous along the tile
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int m16 = lane & 15, q = lane >> 4;
     const bool glu = MODE == MM_FWD && a.act == MM_SWIGLU;
@@ -56,66 +49,88 @@ __global__ __launch_bounds__(256) void ms_kernel(MmArgs a, int tiles_m) {
     // columns 4 * (tid % 16)
     const int sr = tid >> 3, sc = (tid & 7) * 4;
     const int tk = tid >> 4, tc = (tid & 15) * 4;
+    // (rows and columns past the tile's end read the last one: what they give
+    // is not stored)
     const float* arow[2] = {nullptr, nullptr};
     const float* brow[2] = {nullptr, nullptr};
     if constexpr (MODE != MM_WGRAD) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int r = sr + 32 * i;
+            const int r = ch.row0 + min(sr + 32 * i, ch.n - 1);
             if constexpr (MODE == MM_FWD) {
-                if (r < ch.n) arow[i] = x + (size_t)mm_src(a, ch.row0 + r) * a.ldx;
-                const int n = mm_col(a, glu, tn, r);
-                if (n >= 0) brow[i] = wg + (size_t)n * a.ldw;
+                arow[i] = x + (size_t)mm_src(a, r) * a.ldx;
+                const int n = mm_col(a, glu, tn, sr + 32 * i);
+                brow[i] = wg + (size_t)(n < 0 ? a.N - 1 : n) * a.ldw;
             } else {
-                if (r < ch.n) arow[i] = dz + (size_t)(ch.row0 + r) * a.lddz;
+                arow[i] = dz + (size_t)r * a.lddz;
             }
         }
     }
-    f32x4 av[2], bv[2];
-    auto load = [&](int k0) {
+    const int acol = min(m0 + tc, (a.N - 1) & ~3), bcol = min(tn + tc, (a.K - 1) & ~3), klast = (kdim - 1) & ~3;
+    // two stages of pieces in flight; wgrad's x rows (through the pair ids) are
+    // known a stage before their pieces are asked for
+    f32x4 av[2][2], bv[2][2];
+    int src[2] = {0, 0};
+    auto rows_of = [&](int k0) {
+        if constexpr (MODE == MM_WGRAD) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            av[i] = bv[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            const int kr = k0 + tk + 16 * i;
-            if constexpr (MODE == MM_WGRAD) {
-                if (kr < kdim) {
-                    av[i] = ms_ld4(dz + (size_t)(ch.row0 + kr) * a.lddz, m0 + tc, a.N);
-                    bv[i] = ms_ld4(x + (size_t)mm_src(a, ch.row0 + kr) * a.ldx, tn + tc, a.K);
-                }
-            } else {
-                if (arow[i]) av[i] = ms_ld4(arow[i], k0 + sc, kdim);
-                if constexpr (MODE == MM_FWD) {
-                    if (brow[i]) bv[i] = ms_ld4(brow[i], k0 + sc, kdim);
-                } else {
-                    if (kr < kdim) bv[i] = ms_ld4(wg + (size_t)kr * a.ldw, tn + tc, a.K);
-                }
-            }
+            for (int i = 0; i < 2; ++i) src[i] = mm_src(a, ch.row0 + min(k0 + tk + 16 * i, kdim - 1));
         }
     };
-    auto store = [&](int b) {
+    // whole 16-byte pieces without a branch (which would make the compiler wait
+    // for the loads); store() puts zeros behind the contraction's end
+    auto load = [&](int u, int k0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+            const int kr = min(k0 + tk + 16 * i, kdim - 1), kc = min(k0 + sc, klast);
+            const float *pa, *pb;
             if constexpr (MODE == MM_WGRAD) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) As[b][tc + j][tk + 16 * i] = av[i][j];
+                pa = dz + (size_t)(ch.row0 + kr) * a.lddz + acol;
+                pb = x + (size_t)src[i] * a.ldx + bcol;
             } else {
-                *reinterpret_cast<f32x4*>(&As[b][sr + 32 * i][sc]) = av[i];
+                pa = arow[i] + kc;
+                pb = MODE == MM_FWD ? brow[i] + kc : wg + (size_t)kr * a.ldw + bcol;
             }
-            if constexpr (MODE == MM_FWD) {
-                *reinterpret_cast<f32x4*>(&Bs[b][sr + 32 * i][sc]) = bv[i];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) Bs[b][tc + j][tk + 16 * i] = bv[i][j];
-            }
+            av[u][i] = *reinterpret_cast<const f32x4*>(pa);
+            bv[u][i] = *reinterpret_cast<const f32x4*>(pb);
         }
+    };
+    auto store = [&](int b, int k0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (k0 + MS_K > kdim) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool kc = k0 + sc + j < kdim, kr = k0 + tk + 16 * i < kdim;
+                    av[b][i][j] = (AT ? kr : kc) ? av[b][i][j] : 0.0f;
+                    bv[b][i][j] = (BT ? kr : kc) ? bv[b][i][j] : 0.0f;
+                }
+            }
+            *reinterpret_cast<f32x4*>(&As[b][AT ? (tk + 16 * i) * MS_LT + tc : (sr + 32 * i) * MS_LD + sc]) = av[b][i];
+            *reinterpret_cast<f32x4*>(&Bs[b][BT ? (tk + 16 * i) * MS_LT + tc : (sr + 32 * i) * MS_LD + sc]) = bv[b][i];
+        }
+    };
+    // tile row r, contraction columns k .. k+3
+    auto frag = [&](const float* buf, bool t, int r, int k) {
+        if (!t) return *reinterpret_cast<const f32x4*>(buf + r * MS_LD + k);
+        f32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = buf[(k + j) * MS_LT + r];
+        return v;
     };
     f32x4 acc[2][2] = {};
     const int wm = (w & 1) * 32, wn = (w >> 1) * 32;
-    load(0);
-    int b = 0;
-    for (int k0 = 0; k0 < kdim; k0 += MS_K, b ^= 1) {
-        store(b);
-        load(k0 + MS_K);   // (zeros past the end)
+    if (kdim > 0) {
+        rows_of(0);
+        load(0, 0);
+        rows_of(MS_K);
+        load(1, MS_K);
+        rows_of(2 * MS_K);
+    }
+    auto stage = [&](int b, int k0) {
+        store(b, k0);
+        load(b, k0 + 2 * MS_K);
+        rows_of(k0 + 3 * MS_K);
         __syncthreads();
         // lane quarter q holds 4 contraction columns of each half; instruction
         // j takes column j of every quarter (the same for A and B)
@@ -124,8 +139,8 @@ __global__ __launch_bounds__(256) void ms_kernel(MmArgs a, int tiles_m) {
             f32x4 af[2], bf[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                af[i] = *reinterpret_cast<const f32x4*>(&As[b][wm + 16 * i + m16][16 * h + 4 * q]);
-                bf[i] = *reinterpret_cast<const f32x4*>(&Bs[b][wn + 16 * i + m16][16 * h + 4 * q]);
+                af[i] = frag(As[b], AT, wm + 16 * i + m16, 16 * h + 4 * q);
+                bf[i] = frag(Bs[b], BT, wn + 16 * i + m16, 16 * h + 4 * q);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -135,6 +150,10 @@ __global__ __launch_bounds__(256) void ms_kernel(MmArgs a, int tiles_m) {
                     for (int l = 0; l < 2; ++l)
                         acc[i][l] = __builtin_amdgcn_mfma_f32_16x16x4f32(af[i][j], bf[l][j], acc[i][l], 0, 0, 0);
         }
+    };
+    for (int k0 = 0; k0 < kdim; k0 += 2 * MS_K) {
+        stage(0, k0);
+        if (k0 + MS_K < kdim) stage(1, k0 + MS_K);
     }
     // lane: tile column m16, tile rows 4q + t of each 16 x 16 block
 #pragma unroll
