@@ -10,17 +10,26 @@
 //
 // A workgroup computes BR x BC outputs in stages of 64 contraction columns,
 // which global_load_lds_dwordx4 brings into a ring of LDS buffers without
-// passing through registers.  Fragments are read one step of 32 columns ahead
-// of the matrix instructions that take them.  One barrier per stage, in its
-// middle: there every wave has read the stage, whose buffer the next request
-// fills, and the stage after it has landed.
+// passing through registers.  One barrier per stage: behind it the stage's
+// buffer may be filled again, and a later stage has landed.  In the 256-wide
+// tiles, one workgroup per CU, fragments are read one step of 32 columns ahead
+// of the matrix instructions that take them and the barrier stands in the
+// stage's middle (dgrad 129 -> 113 us, wgrad 134 -> 117 us at 4096 x 7168 x
+// 2048); of the smaller ones several share a CU and cover each other's waits.
 //   Contiguous along k: tile row r is 128 bytes, its 16-byte chunk c in slot
 //     c ^ ((r >> 1) & 7), so a fragment read (16 rows at one chunk per lane
 //     quarter, ds_read_b128) covers all 64 banks.
 //   Contiguous along the tile: contraction row k is one LDS row, its 32-byte
 //     granule g (16 columns) in place g ^ (k & 3 | (k >> 3 & 1) << 2) (64
-//     columns: g ^ (k >> 1 & 1 | (k >> 3 & 1) << 1)); the fragment is read transposed (ds_read_b64_tr_b16: 16 lanes take 4
-//     contraction rows x 16 columns, and a lane gets its column's 4 values).
+//     columns: g ^ (k >> 1 & 1 | (k >> 3 & 1) << 1)); the fragment is read
+//     transposed (ds_read_b64_tr_b16: 16 lanes take 4 contraction rows x 16
+//     columns, and a lane gets its column's 4 values).
+// Counters: no LDS bank conflicts in any mode; at 256 x 256 matrix cores busy
+// 61% (forward), 49% (dgrad) and 46% (wgrad) of the cycles.  1.2 PFLOP/s at 4096
+// x 7168 -> 4096 with SwiGLU (203 us; the library's plain product 169), 1.06
+// over dx and dW of 4096 rows, 7168 -> 2048 (112 + 116 us).  Groups of few rows
+// are bound by their weights (4096 tokens' down products of 256 experts at 4.1
+// TB/s), their dW by each tile's start and writing (25% busy).
 // The column operand goes first into the matrix instruction, so a lane holds 4
 // consecutive columns of one row of C; they leave through LDS in whole rows.
 #include "matmul.hpp"
