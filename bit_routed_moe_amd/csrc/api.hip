@@ -305,9 +305,8 @@ bool batch1_path(const ds4moe_config* cfg, int32_t T) {
 
 // ---- products at original precision ---------------------------------------------
 
-// Largest product of two of a call's sizes: grids and element counts stay
-// below 2^32 workgroups' threads at the smallest tiles (64 x 64).
-constexpr int64_t MM_MAX_ELEMS = (int64_t)1 << 36;
+// Most 64 x 64 tiles (the smallest) of a launch: its threads stay below 2^32.
+constexpr int64_t MM_MAX_TILES = (int64_t)1 << 23;
 
 int check_ld(const char* name, int64_t ld, int64_t cols, int64_t q) {
     if (ld < cols) return fail(DS4MOE_E_SHAPE, "%s %lld is below the row's %lld elements", name, (long long)ld,
@@ -338,10 +337,11 @@ int check_mm(const ds4moe_matmul* m, int32_t rows) {
         return fail(DS4MOE_E_SHAPE, "SwiGLU needs an even out_dim, not %d", m->out_dim);
     if (m->groups < 1 || m->groups > 1024) return fail(DS4MOE_E_SHAPE, "groups %d not in [1, 1024]", m->groups);
     if (rows < 1 || rows > (1 << 24)) return fail(DS4MOE_E_SHAPE, "rows %d not in [1, 2^24]", rows);
-    if ((int64_t)rows * m->in_dim > MM_MAX_ELEMS || (int64_t)rows * m->out_dim > MM_MAX_ELEMS ||
-        (int64_t)m->in_dim * m->out_dim > MM_MAX_ELEMS)
-        return fail(DS4MOE_E_SHAPE, "%d rows of %d x %d: a product of two sizes is above 2^36", rows, m->out_dim,
-                    m->in_dim);
+    const int64_t rt = rows / 64 + (m->groups < rows ? m->groups : rows) + 1;
+    const int64_t kt = m->in_dim / 64 + 1, nt = m->out_dim / 64 + 1;
+    if (rt * kt > MM_MAX_TILES || rt * nt > MM_MAX_TILES || kt * nt > MM_MAX_TILES)
+        return fail(DS4MOE_E_SHAPE, "%d rows in %d groups of %d x %d: more than 2^23 tiles", rows, m->groups,
+                    m->out_dim, m->in_dim);
     return DS4MOE_OK;
 }
 

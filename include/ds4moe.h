@@ -327,8 +327,9 @@ int ds4moe_quantize_mxfp8(const void* x_bf16, int64_t n, uint8_t* codes, uint8_t
  *       tensor's allocation).  Experts follow one another at
  *       out_dim * ldw; bias and dbias [groups][out_dim] have no gaps.
  * Limits: 1 <= in_dim, out_dim <= 2^20, 1 <= groups <= 1024,
- *       1 <= rows <= 2^24, and rows * in_dim, rows * out_dim and
- *       out_dim * in_dim each at most 2^36 (else DS4MOE_E_SHAPE).
+ *       1 <= rows <= 2^24, and of the three numbers of 64-wide tiles
+ *       rows/64 + min(groups, rows) + 1, in_dim/64 + 1 and out_dim/64 + 1 any
+ *       two multiply to at most 2^23 (else DS4MOE_E_SHAPE).
  * Outputs must not overlap inputs, except that y may be residual itself. */
 typedef enum {
     DS4MOE_ACT_NONE = 0, DS4MOE_ACT_RELU = 1, DS4MOE_ACT_SILU = 2, DS4MOE_ACT_GELU = 3,

@@ -36,8 +36,11 @@ def test_descriptor():
     assert lin(mk((1 << 20) + 8, 8)) == -2 and lin(mk(8, (1 << 20) + 1)) == -2
     assert lin(mk(64, 64), rows=0) == -2 and lin(mk(64, 64), rows=-1) == -2
     assert lin(mk(64, 64), rows=(1 << 24) + 1) == -2
-    assert lin(mk(1 << 20, 64), rows=1 << 20) == -2          # rows * in_dim above 2^36
+    assert lin(mk(1 << 20, 64), rows=1 << 20) == -2          # more tiles than a launch takes
     assert lin(mk(1 << 20, 1 << 20)) == -2
+    assert lin(mk(64, 1 << 20), rows=1 << 16) == -2
+    assert grp(mk(64, 1 << 20, groups=1024), rows=4096, x_rows=4096) == -2
+    assert grp(mk(64, 1 << 18, groups=1024), rows=4096, x_rows=4096, x=MIS) == -3
     assert lin(mk(64, 64, groups=2)) == -2                   # linear: one group
     assert grp(mk(64, 64, groups=0)) == -2 and grp(mk(64, 64, groups=1025)) == -2
     assert lin(mk(64, 65, act="swiglu")) == -2
