@@ -130,11 +130,12 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _s(stream):
+def _s(stream, dev=None):
+    """Handle of a stream; None: the current one (of device `dev`, where its index is at hand)."""
     if stream is not None:
         return ctypes.c_void_p(stream if isinstance(stream, int) else stream.cuda_stream)
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
 def make_config(hidden, ffn, n_experts, top_k, shared_ffn=0, wfmt="q2k", act="bf16", mma="bf16",
@@ -259,6 +260,24 @@ def _d(*tensors):
     return [None if t is None else t.data_ptr() for t in tensors]
 
 
+def _here():
+    """Index of the current HIP device, None without one."""
+    import torch
+    cuda = torch.cuda
+    return cuda.current_device() if cuda.is_initialized() or cuda.is_available() else None
+
+
+def _vector(name, t, dtype, dev):
+    """Device pointer of a tensor of `dtype` on device `dev` (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise Ds4MoeError(-1, f"{name} is {t.dtype}, not {dtype}")
+    if t.get_device() != dev:
+        raise Ds4MoeError(-1, f"{name} on {t.device}, not on the current HIP device {dev}")
+    return t.data_ptr()
+
+
 def _ws(workspace):
     return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
@@ -309,11 +328,17 @@ def sample(B, V, logits, u, token, temperature=None, top_k=None, top_p=None, min
            stream=None):
     """token[B] (and prob[B]) sampled from logits [B][V] (fp32 or bf16; rows may
     be logits.stride(0) apart) with the random numbers u[B]; the filters' values
-    are per row, None switches one off."""
+    are per row, None switches one off.  top_k and token are int32, the other
+    vectors fp32; anything else is refused."""
     import torch
-    dtype = {torch.float32: 0, torch.bfloat16: 1}.get(logits.dtype)
-    if dtype is None or logits.stride(-1) != 1:
+    f32, i32, dev = torch.float32, torch.int32, _here()
+    if logits.dtype not in (f32, torch.bfloat16) or logits.stride(-1) != 1:
         raise Ds4MoeError(-1, f"logits {logits.dtype} with strides {logits.stride()}")
-    pl, pt, pk, pp, pm, pu, po, pr, ps = _d(logits, temperature, top_k, top_p, min_p, u, token, prob, workspace)
-    _check(lib.ds4moe_sample(B, V, pl, logits.stride(0) if B > 1 else V, dtype, pt, pk, pp, pm, pu, po, pr, ps,
-                             _ws(workspace), _s(stream)))
+    dtype = 0 if logits.dtype == f32 else 1
+    _check(lib.ds4moe_sample(
+        B, V, _vector("logits", logits, logits.dtype, dev), logits.stride(0) if B > 1 else V, dtype,
+        _vector("temperature", temperature, f32, dev), _vector("top_k", top_k, i32, dev),
+        _vector("top_p", top_p, f32, dev), _vector("min_p", min_p, f32, dev), _vector("u", u, f32, dev),
+        _vector("token", token, i32, dev), _vector("prob", prob, f32, dev),
+        None if workspace is None else _vector("workspace", workspace, workspace.dtype, dev), _ws(workspace),
+        _s(stream, dev)))

@@ -1,0 +1,61 @@
+"""The Python binding refuses tensors that its descriptor or its arguments do
+not describe, before the library is called.  No GPU: the library is replaced by
+a recorder, and tensors on the host stand for those on the current device."""
+import pytest
+import torch
+
+ds4 = pytest.importorskip("bit_routed_moe_amd")
+
+ARG, SHAPE = -1, -2
+
+
+class Recorder:
+    """In place of the library: every entry point notes its name and succeeds."""
+
+    def __init__(self):
+        self.called = []
+
+    def __getattr__(self, name):
+        return lambda *args: self.called.append(name) or 0
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(ds4, "lib", r)
+    monkeypatch.setattr(ds4, "_here", lambda: -1, raising=False)   # (a host tensor's device index)
+    monkeypatch.setattr(ds4, "_s", lambda *args: None)
+    return r
+
+
+def refused(lib, status, match, fn, *args, **kw):
+    with pytest.raises(ds4.Ds4MoeError, match=match) as e:
+        fn(*args, **kw)
+    assert e.value.status == status and not lib.called
+
+
+def accepted(lib, fn, *args, **kw):
+    fn(*args, **kw)
+    assert len(lib.called) == 1
+    lib.called.clear()
+
+
+# ---- sample ----------------------------------------------------------------------
+
+def sample_args(B=3, V=50):
+    a = dict(logits=torch.zeros(B, V), u=torch.zeros(B), token=torch.zeros(B, dtype=torch.int32),
+             temperature=torch.ones(B), top_k=torch.ones(B, dtype=torch.int32), top_p=torch.ones(B),
+             min_p=torch.zeros(B), prob=torch.zeros(B))
+    return B, V, a
+
+
+def test_sample_types(lib):
+    B, V, a = sample_args()
+    accepted(lib, ds4.sample, B, V, **a)
+    accepted(lib, ds4.sample, B, V, **dict(a, logits=a["logits"].bfloat16()))
+    for n in ("temperature", "top_k", "top_p", "min_p", "prob"):
+        accepted(lib, ds4.sample, B, V, **dict(a, **{n: None}))
+    for n, t in a.items():
+        for dt in (torch.int64, torch.float64, torch.float16, torch.int32, torch.float32):
+            if dt != t.dtype and not (n == "logits" and dt == torch.float32):
+                refused(lib, ARG, f"{n} (is )?{dt}", ds4.sample, B, V, **dict(a, **{n: t.to(dt)}))
