@@ -267,12 +267,15 @@ def _here():
     return cuda.current_device() if cuda.is_initialized() or cuda.is_available() else None
 
 
-def _vector(name, t, dtype, dev):
-    """Device pointer of a tensor of `dtype` on device `dev` (None: NULL)."""
+def _vector(name, t, dtype, n, dev):
+    """Device pointer of at least `n` contiguous elements of `dtype` on device
+    `dev` (None: NULL)."""
     if t is None:
         return None
     if t.dtype != dtype:
         raise Ds4MoeError(-1, f"{name} is {t.dtype}, not {dtype}")
+    if t.numel() < n or not t.is_contiguous():
+        raise Ds4MoeError(-2, f"{name} of shape {tuple(t.shape)}, strides {t.stride()}: not {n} contiguous elements")
     if t.get_device() != dev:
         raise Ds4MoeError(-1, f"{name} on {t.device}, not on the current HIP device {dev}")
     return t.data_ptr()
@@ -329,16 +332,23 @@ def sample(B, V, logits, u, token, temperature=None, top_k=None, top_p=None, min
     """token[B] (and prob[B]) sampled from logits [B][V] (fp32 or bf16; rows may
     be logits.stride(0) apart) with the random numbers u[B]; the filters' values
     are per row, None switches one off.  top_k and token are int32, the other
-    vectors fp32; anything else is refused."""
+    vectors fp32, all contiguous; anything else, or fewer rows or tokens than B
+    and V, is refused."""
     import torch
     f32, i32, dev = torch.float32, torch.int32, _here()
     if logits.dtype not in (f32, torch.bfloat16) or logits.stride(-1) != 1:
         raise Ds4MoeError(-1, f"logits {logits.dtype} with strides {logits.stride()}")
-    dtype = 0 if logits.dtype == f32 else 1
+    dtype, ld = 0 if logits.dtype == f32 else 1, V
+    if logits.size(-1) < V or logits.size(0) < (B if logits.dim() > 1 else B * V):
+        raise Ds4MoeError(-2, f"logits of shape {tuple(logits.shape)} for {B} rows of {V}")
+    if B > 1:
+        ld = logits.stride(0)
+    if logits.get_device() != dev:
+        raise Ds4MoeError(-1, f"logits on {logits.device}, not on the current HIP device {dev}")
     _check(lib.ds4moe_sample(
-        B, V, _vector("logits", logits, logits.dtype, dev), logits.stride(0) if B > 1 else V, dtype,
-        _vector("temperature", temperature, f32, dev), _vector("top_k", top_k, i32, dev),
-        _vector("top_p", top_p, f32, dev), _vector("min_p", min_p, f32, dev), _vector("u", u, f32, dev),
-        _vector("token", token, i32, dev), _vector("prob", prob, f32, dev),
-        None if workspace is None else _vector("workspace", workspace, workspace.dtype, dev), _ws(workspace),
+        B, V, logits.data_ptr(), ld, dtype, _vector("temperature", temperature, f32, B, dev),
+        _vector("top_k", top_k, i32, B, dev), _vector("top_p", top_p, f32, B, dev),
+        _vector("min_p", min_p, f32, B, dev), _vector("u", u, f32, B, dev), _vector("token", token, i32, B, dev),
+        _vector("prob", prob, f32, B, dev),
+        None if workspace is None else _vector("workspace", workspace, workspace.dtype, 0, dev), _ws(workspace),
         _s(stream, dev)))

@@ -59,3 +59,27 @@ def test_sample_types(lib):
         for dt in (torch.int64, torch.float64, torch.float16, torch.int32, torch.float32):
             if dt != t.dtype and not (n == "logits" and dt == torch.float32):
                 refused(lib, ARG, f"{n} (is )?{dt}", ds4.sample, B, V, **dict(a, **{n: t.to(dt)}))
+
+
+def test_sample_sizes(lib):
+    B, V, a = sample_args()
+    for n, t in a.items():
+        if n != "logits":
+            refused(lib, SHAPE, n, ds4.sample, B, V, **dict(a, **{n: t[:-1]}))
+            refused(lib, SHAPE, n, ds4.sample, B, V, **dict(a, **{n: t[:1].expand(B)}))         # one value in memory
+            refused(lib, SHAPE, n, ds4.sample, B, V, **dict(a, **{n: torch.stack([t, t], 1)[:, 0]}))
+            accepted(lib, ds4.sample, B, V, **dict(a, **{n: torch.cat([t, t])}))                # room for more rows
+            accepted(lib, ds4.sample, B, V, **dict(a, **{n: t[:, None]}))
+    for bad in (torch.zeros(B, V - 1), torch.zeros(B - 1, V), torch.zeros(2, 3, V)[:, 0], torch.zeros(1, B, V)):
+        refused(lib, SHAPE, "logits", ds4.sample, B, V, **dict(a, logits=bad))
+    for good in (torch.zeros(B + 1, V), torch.zeros(B, V + 6)[:, :V], torch.zeros(B, V + 6), torch.zeros(B, 1, V)):
+        accepted(lib, ds4.sample, B, V, **dict(a, logits=good))
+
+
+def test_sample_one_row(lib):
+    _, V, a = sample_args(1)
+    accepted(lib, ds4.sample, 1, V, **dict(a, logits=torch.zeros(V)))
+    accepted(lib, ds4.sample, 1, V, **dict(a, temperature=torch.tensor(0.7)))       # no dimension: one value
+    refused(lib, SHAPE, "logits", ds4.sample, 1, V, **dict(a, logits=torch.zeros(V - 1)))
+    refused(lib, SHAPE, "logits", ds4.sample, 1, V, **dict(a, logits=torch.zeros(0, V)))
+    refused(lib, SHAPE, "logits", ds4.sample, 3, 1, torch.zeros(1), torch.zeros(3), torch.zeros(3, dtype=torch.int32))
