@@ -250,16 +250,6 @@ def matmul_workspace_bytes(m: Matmul, rows: int, backward: bool = False) -> int:
     return int(lib.ds4moe_matmul_workspace_bytes(ctypes.byref(m), rows, int(backward)))
 
 
-def _d(*tensors):
-    """Device pointers of tensors (or None), all on the current HIP device."""
-    import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
-            raise Ds4MoeError(-1, f"tensor on {t.device}, not on the current HIP device {dev}")
-    return [None if t is None else t.data_ptr() for t in tensors]
-
-
 def _here():
     """Index of the current HIP device, None without one."""
     import torch
@@ -285,28 +275,60 @@ def _ws(workspace):
     return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
+def _operand(name, t, dtype, dev):
+    """Device pointer of a tensor of `dtype` (None: the library refuses the
+    descriptor) on device `dev`."""
+    if t is None:
+        return None
+    if t.dtype != dtype and dtype is not None:
+        raise Ds4MoeError(-1, f"{name} is {t.dtype}, not {dtype}")
+    if t.get_device() != dev:
+        raise Ds4MoeError(-1, f"{name} on {t.device}, not on the current HIP device {dev}")
+    return t.data_ptr()
+
+
+def _mm_types(m):
+    """Types of a descriptor's tensors and of their gradients, and the current device."""
+    import torch
+    types = (torch.float32, torch.bfloat16)
+    return (types[m.dtype] if 0 <= m.dtype <= 1 else None, types[m.grad_dtype] if 0 <= m.grad_dtype <= 1 else None,
+            torch.int32, _here())
+
+
 def linear(m, rows, x, w, y, bias=None, residual=None, z=None, workspace=None, stream=None):
-    """y = act(x W^T + bias) + residual; z (optional) receives the pre-activations."""
-    px, pw, pb, pr, py, pz, ps = _d(x, w, bias, residual, y, z, workspace)
-    _check(lib.ds4moe_linear(ctypes.byref(m), rows, px, pw, pb, pr, py, pz, ps, _ws(workspace), _s(stream)))
+    """y = act(x W^T + bias) + residual; z (optional) receives the pre-activations.
+    Tensors of other types than the descriptor's are refused."""
+    dt, _, _, dev = _mm_types(m)
+    _check(lib.ds4moe_linear(
+        ctypes.byref(m), rows, _operand("x", x, dt, dev), _operand("w", w, dt, dev), _operand("bias", bias, dt, dev),
+        _operand("residual", residual, dt, dev), _operand("y", y, dt, dev), _operand("z", z, dt, dev),
+        _operand("workspace", workspace, None, dev), _ws(workspace), _s(stream, dev)))
 
 
 def linear_backward(m, rows, x, w, dy, z=None, dx=None, dw=None, dbias=None, workspace=None, stream=None):
     """Gradients of linear: each of dx, dw, dbias that is given."""
-    px, pw, pz, pdy, pdx, pdw, pdb, ps = _d(x, w, z, dy, dx, dw, dbias, workspace)
-    _check(lib.ds4moe_linear_backward(ctypes.byref(m), rows, px, pw, pz, pdy, pdx, pdw, pdb, ps, _ws(workspace),
-                                      _s(stream)))
+    dt, gd, _, dev = _mm_types(m)
+    # (what the call does not read may be anything)
+    x, w, z = None if dw is None else x, None if dx is None else w, z if m.act else None
+    _check(lib.ds4moe_linear_backward(
+        ctypes.byref(m), rows, _operand("x", x, dt, dev), _operand("w", w, dt, dev), _operand("z", z, dt, dev),
+        _operand("dy", dy, dt, dev), _operand("dx", dx, dt, dev), _operand("dw", dw, gd, dev),
+        _operand("dbias", dbias, gd, dev), _operand("workspace", workspace, None, dev), _ws(workspace),
+        _s(stream, dev)))
 
 
 def grouped_matmul(m, rows, x, w, expert_offsets, y, sorted_pair=None, top_k=1, x_rows=None, bias=None, z=None,
                    workspace=None, stream=None):
     """Products of expert-sorted rows with their experts' weights, from
     permute's expert_offsets (and sorted_pair, when rows are read from the
-    tokens' x)."""
-    px, pw, pb, po, pp, py, pz, ps = _d(x, w, bias, expert_offsets, sorted_pair, y, z, workspace)
+    tokens' x), both int32."""
+    dt, _, i32, dev = _mm_types(m)
     xr = x.shape[0] if x_rows is None else x_rows
-    _check(lib.ds4moe_grouped_matmul(ctypes.byref(m), rows, px, xr, pw, pb, po, pp, top_k, py, pz, ps,
-                                     _ws(workspace), _s(stream)))
+    _check(lib.ds4moe_grouped_matmul(
+        ctypes.byref(m), rows, _operand("x", x, dt, dev), xr, _operand("w", w, dt, dev),
+        _operand("bias", bias, dt, dev), _operand("expert_offsets", expert_offsets, i32, dev),
+        _operand("sorted_pair", sorted_pair, i32, dev), top_k, _operand("y", y, dt, dev), _operand("z", z, dt, dev),
+        _operand("workspace", workspace, None, dev), _ws(workspace), _s(stream, dev)))
 
 
 def grouped_matmul_backward(m, rows, x, w, expert_offsets, dy, z=None, sorted_pair=None, top_k=1, x_rows=None,
@@ -314,11 +336,15 @@ def grouped_matmul_backward(m, rows, x, w, expert_offsets, dy, z=None, sorted_pa
     """Gradients of grouped_matmul: each of dx (a row per sorted row), dw,
     dbias that is given.  x is read for dw only, but its row count is always
     part of the call (x_rows, if x is None)."""
-    px, pw, pz, pdy, po, pp, pdx, pdw, pdb, ps = _d(x, w, z, dy, expert_offsets, sorted_pair, dx, dw, dbias,
-                                                    workspace)
+    dt, gd, i32, dev = _mm_types(m)
     xr = x_rows if x_rows is not None else (x.shape[0] if x is not None else rows)
-    _check(lib.ds4moe_grouped_matmul_backward(ctypes.byref(m), rows, px, xr, pw, pz, pdy, po, pp, top_k, pdx, pdw,
-                                              pdb, ps, _ws(workspace), _s(stream)))
+    x, w, z = None if dw is None else x, None if dx is None else w, z if m.act else None
+    _check(lib.ds4moe_grouped_matmul_backward(
+        ctypes.byref(m), rows, _operand("x", x, dt, dev), xr, _operand("w", w, dt, dev), _operand("z", z, dt, dev),
+        _operand("dy", dy, dt, dev), _operand("expert_offsets", expert_offsets, i32, dev),
+        _operand("sorted_pair", sorted_pair, i32, dev), top_k, _operand("dx", dx, dt, dev),
+        _operand("dw", dw, gd, dev), _operand("dbias", dbias, gd, dev), _operand("workspace", workspace, None, dev),
+        _ws(workspace), _s(stream, dev)))
 
 
 # ---- token sampling ------------------------------------------------------------
@@ -350,5 +376,5 @@ def sample(B, V, logits, u, token, temperature=None, top_k=None, top_p=None, min
         _vector("top_k", top_k, i32, B, dev), _vector("top_p", top_p, f32, B, dev),
         _vector("min_p", min_p, f32, B, dev), _vector("u", u, f32, B, dev), _vector("token", token, i32, B, dev),
         _vector("prob", prob, f32, B, dev),
-        None if workspace is None else _vector("workspace", workspace, workspace.dtype, 0, dev), _ws(workspace),
+        _operand("workspace", workspace, None, dev), _ws(workspace),
         _s(stream, dev)))

@@ -83,3 +83,46 @@ def test_sample_one_row(lib):
     refused(lib, SHAPE, "logits", ds4.sample, 1, V, **dict(a, logits=torch.zeros(V - 1)))
     refused(lib, SHAPE, "logits", ds4.sample, 1, V, **dict(a, logits=torch.zeros(0, V)))
     refused(lib, SHAPE, "logits", ds4.sample, 3, 1, torch.zeros(1), torch.zeros(3), torch.zeros(3, dtype=torch.int32))
+
+
+# ---- products --------------------------------------------------------------------
+
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def product(dtype="bf16", grad=None, act="none", groups=None, rows=6, K=24, N=16, pad=0):
+    """Descriptor and tensors of a product (rows at `pad` elements behind one another's ends)."""
+    t, g = (BF if dtype == "bf16" else F32), (F32 if (grad or dtype) == "f32" else BF)
+    E, oc = groups or 1, N // 2 if act == "swiglu" else N
+    m = ds4.make_matmul(K, N, groups=E, dtype=dtype, grad=grad, act=act, ldx=K + pad, ldw=K + pad, ldy=oc + pad,
+                        ldz=N + pad)
+    mk = lambda r, c, dt: torch.zeros(*r, c + pad, dtype=dt)[..., :c]
+    a = dict(x=mk((rows,), K, t), w=mk((E, N), K, t), bias=torch.zeros(E, N, dtype=t), y=mk((rows,), oc, t),
+             z=mk((rows,), N, t), residual=mk((rows,), oc, t), dy=mk((rows,), oc, t), dx=mk((rows,), K, t),
+             dw=mk((E, N), K, g), dbias=torch.zeros(E, N, dtype=g),
+             expert_offsets=torch.zeros(E + 1, dtype=I32), sorted_pair=torch.zeros(rows, dtype=I32))
+    return m, rows, a
+
+
+FORWARD = ("x", "w", "y", "bias", "residual", "z")
+BACKWARD = ("x", "w", "dy", "z", "dx", "dw", "dbias")
+GROUPED = ("x", "w", "expert_offsets", "y", "bias", "z", "sorted_pair")
+GROUPED_BACKWARD = ("x", "w", "expert_offsets", "dy", "z", "dx", "dw", "dbias", "sorted_pair")
+CALLS = [("linear", FORWARD, None), ("linear_backward", BACKWARD, None), ("grouped_matmul", GROUPED, 3),
+         ("grouped_matmul_backward", GROUPED_BACKWARD, 3)]
+
+
+def pick(a, names):
+    return {n: a[n] for n in names}
+
+
+@pytest.mark.parametrize("fn,names,groups", CALLS, ids=[c[0] for c in CALLS])
+@pytest.mark.parametrize("dtype,grad", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_product_types(lib, fn, names, groups, dtype, grad):
+    m, rows, a = product(dtype, grad, "silu", groups)
+    call, a = getattr(ds4, fn), pick(a, names)
+    accepted(lib, call, m, rows, **a)
+    for n, t in a.items():
+        for dt in (torch.int64, torch.float64, torch.float16, torch.int32, torch.float32, torch.bfloat16):
+            if dt != t.dtype:
+                refused(lib, ARG, f"{n} is {dt}", call, m, rows, **dict(a, **{n: t.to(dt)}))
