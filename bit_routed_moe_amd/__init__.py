@@ -262,7 +262,7 @@ def _vector(name, t, dtype, n, dev):
     `dev` (None: NULL)."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype != dtype and dtype is not None:   # (None: the library refuses the descriptor)
         raise Ds4MoeError(-1, f"{name} is {t.dtype}, not {dtype}")
     if t.numel() < n or not t.is_contiguous():
         raise Ds4MoeError(-2, f"{name} of shape {tuple(t.shape)}, strides {t.stride()}: not {n} contiguous elements")
@@ -271,64 +271,110 @@ def _vector(name, t, dtype, n, dev):
     return t.data_ptr()
 
 
-def _ws(workspace):
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+def _workspace(t, dev):
+    """Device pointer and bytes of a workspace of any type (None: NULL, 0)."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        raise Ds4MoeError(-2, f"workspace of shape {tuple(t.shape)}, strides {t.stride()} is not contiguous")
+    if t.get_device() != dev:
+        raise Ds4MoeError(-1, f"workspace on {t.device}, not on the current HIP device {dev}")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _operand(name, t, dtype, dev):
-    """Device pointer of a tensor of `dtype` (None: the library refuses the
-    descriptor) on device `dev`."""
+def _rows_apart(shape, strides, rows, cols, ld):
+    """Whether a tensor's first `rows` rows, counted over all its dimensions but
+    the last, are `cols` or more elements that start `ld` apart."""
+    if not shape or (cols > 1 and strides[-1] != 1):
+        return False
+    if len(shape) == 1:                      # memory without rows
+        return shape[0] >= (rows - 1) * ld + cols
+    n = 1
+    for size, stride in zip(shape[-2::-1], strides[-2::-1]):
+        if n < rows and size != 1 and stride != n * ld:
+            return False
+        n *= size
+    return shape[-1] >= cols and n >= rows
+
+
+def _matrix(name, t, dtype, rows, cols, ld, dev):
+    """Device pointer of `rows` rows of `cols` elements of `dtype`, `ld` apart
+    (0: without gaps), on device `dev` (None: NULL).  A tensor may have more
+    rows and columns than that."""
     if t is None:
         return None
-    if t.dtype != dtype and dtype is not None:
+    if t.dtype != dtype and dtype is not None:   # (None: the library refuses the descriptor)
         raise Ds4MoeError(-1, f"{name} is {t.dtype}, not {dtype}")
+    ld = ld or cols
+    # (the ordinary tensor first: this is host time of every call)
+    if not ((t.is_contiguous() and t.dim() > 1 and t.shape[-1] == ld >= cols and t.numel() >= rows * ld)
+            or _rows_apart(t.shape, t.stride(), rows, cols, ld)):
+        raise Ds4MoeError(-2, f"{name} of shape {tuple(t.shape)}, strides {t.stride()}: not {rows} rows of {cols} "
+                              f"elements, {ld} apart")
     if t.get_device() != dev:
         raise Ds4MoeError(-1, f"{name} on {t.device}, not on the current HIP device {dev}")
     return t.data_ptr()
 
 
-def _mm_types(m):
-    """Types of a descriptor's tensors and of their gradients, and the current device."""
+def _mm_plan(m):
+    """A descriptor's types (of its tensors, of their gradients, int32), rows of
+    w, columns of y, and the current device."""
     import torch
     types = (torch.float32, torch.bfloat16)
-    return (types[m.dtype] if 0 <= m.dtype <= 1 else None, types[m.grad_dtype] if 0 <= m.grad_dtype <= 1 else None,
-            torch.int32, _here())
+    dt, gd, n = m.dtype, m.grad_dtype, m.out_dim
+    return (types[dt] if 0 <= dt <= 1 else None, types[gd] if 0 <= gd <= 1 else None, torch.int32, m.groups * n,
+            n // 2 if m.act == ACT["swiglu"] else n, _here())
+
+
+def _x_rows(x, rows):
+    """Rows of x that a grouped call does not state."""
+    if x is None:
+        return rows
+    return x.shape[0] if x.dim() < 2 or x.shape[-1] == 0 else x.numel() // x.shape[-1]
 
 
 def linear(m, rows, x, w, y, bias=None, residual=None, z=None, workspace=None, stream=None):
     """y = act(x W^T + bias) + residual; z (optional) receives the pre-activations.
-    Tensors of other types than the descriptor's are refused."""
-    dt, _, _, dev = _mm_types(m)
+    Tensors whose type, size or row stride is not the descriptor's are refused
+    (a tensor may have more rows and columns); w [.., out_dim, in_dim] and bias
+    are counted over all their leading dimensions."""
+    dt, _, _, wrows, oc, dev = _mm_plan(m)
+    k, n, ldy = m.in_dim, m.out_dim, m.ldy
+    ws, nws = _workspace(workspace, dev)
     _check(lib.ds4moe_linear(
-        ctypes.byref(m), rows, _operand("x", x, dt, dev), _operand("w", w, dt, dev), _operand("bias", bias, dt, dev),
-        _operand("residual", residual, dt, dev), _operand("y", y, dt, dev), _operand("z", z, dt, dev),
-        _operand("workspace", workspace, None, dev), _ws(workspace), _s(stream, dev)))
+        ctypes.byref(m), rows, _matrix("x", x, dt, rows, k, m.ldx, dev), _matrix("w", w, dt, wrows, k, m.ldw, dev),
+        _vector("bias", bias, dt, wrows, dev), _matrix("residual", residual, dt, rows, oc, ldy, dev),
+        _matrix("y", y, dt, rows, oc, ldy, dev), _matrix("z", z, dt, rows, n, m.ldz, dev), ws, nws, _s(stream, dev)))
 
 
 def linear_backward(m, rows, x, w, dy, z=None, dx=None, dw=None, dbias=None, workspace=None, stream=None):
     """Gradients of linear: each of dx, dw, dbias that is given."""
-    dt, gd, _, dev = _mm_types(m)
+    dt, gd, _, wrows, oc, dev = _mm_plan(m)
+    k, n, ldx, ldw = m.in_dim, m.out_dim, m.ldx, m.ldw
     # (what the call does not read may be anything)
     x, w, z = None if dw is None else x, None if dx is None else w, z if m.act else None
+    ws, nws = _workspace(workspace, dev)
     _check(lib.ds4moe_linear_backward(
-        ctypes.byref(m), rows, _operand("x", x, dt, dev), _operand("w", w, dt, dev), _operand("z", z, dt, dev),
-        _operand("dy", dy, dt, dev), _operand("dx", dx, dt, dev), _operand("dw", dw, gd, dev),
-        _operand("dbias", dbias, gd, dev), _operand("workspace", workspace, None, dev), _ws(workspace),
-        _s(stream, dev)))
+        ctypes.byref(m), rows, _matrix("x", x, dt, rows, k, ldx, dev), _matrix("w", w, dt, wrows, k, ldw, dev),
+        _matrix("z", z, dt, rows, n, m.ldz, dev), _matrix("dy", dy, dt, rows, oc, m.ldy, dev),
+        _matrix("dx", dx, dt, rows, k, ldx, dev), _matrix("dw", dw, gd, wrows, k, ldw, dev),
+        _vector("dbias", dbias, gd, wrows, dev), ws, nws, _s(stream, dev)))
 
 
 def grouped_matmul(m, rows, x, w, expert_offsets, y, sorted_pair=None, top_k=1, x_rows=None, bias=None, z=None,
                    workspace=None, stream=None):
     """Products of expert-sorted rows with their experts' weights, from
     permute's expert_offsets (and sorted_pair, when rows are read from the
-    tokens' x), both int32."""
-    dt, _, i32, dev = _mm_types(m)
-    xr = x.shape[0] if x_rows is None else x_rows
+    tokens' x), both int32.  x_rows: x's rows (default: all that it has)."""
+    dt, _, i32, wrows, oc, dev = _mm_plan(m)
+    k, xr = m.in_dim, _x_rows(x, rows) if x_rows is None else x_rows
+    ws, nws = _workspace(workspace, dev)
     _check(lib.ds4moe_grouped_matmul(
-        ctypes.byref(m), rows, _operand("x", x, dt, dev), xr, _operand("w", w, dt, dev),
-        _operand("bias", bias, dt, dev), _operand("expert_offsets", expert_offsets, i32, dev),
-        _operand("sorted_pair", sorted_pair, i32, dev), top_k, _operand("y", y, dt, dev), _operand("z", z, dt, dev),
-        _operand("workspace", workspace, None, dev), _ws(workspace), _s(stream, dev)))
+        ctypes.byref(m), rows, _matrix("x", x, dt, xr, k, m.ldx, dev), xr,
+        _matrix("w", w, dt, wrows, k, m.ldw, dev), _vector("bias", bias, dt, wrows, dev),
+        _vector("expert_offsets", expert_offsets, i32, m.groups + 1, dev),
+        _vector("sorted_pair", sorted_pair, i32, rows, dev), top_k, _matrix("y", y, dt, rows, oc, m.ldy, dev),
+        _matrix("z", z, dt, rows, m.out_dim, m.ldz, dev), ws, nws, _s(stream, dev)))
 
 
 def grouped_matmul_backward(m, rows, x, w, expert_offsets, dy, z=None, sorted_pair=None, top_k=1, x_rows=None,
@@ -336,15 +382,16 @@ def grouped_matmul_backward(m, rows, x, w, expert_offsets, dy, z=None, sorted_pa
     """Gradients of grouped_matmul: each of dx (a row per sorted row), dw,
     dbias that is given.  x is read for dw only, but its row count is always
     part of the call (x_rows, if x is None)."""
-    dt, gd, i32, dev = _mm_types(m)
-    xr = x_rows if x_rows is not None else (x.shape[0] if x is not None else rows)
+    dt, gd, i32, wrows, oc, dev = _mm_plan(m)
+    k, ldx, ldw, xr = m.in_dim, m.ldx, m.ldw, _x_rows(x, rows) if x_rows is None else x_rows
     x, w, z = None if dw is None else x, None if dx is None else w, z if m.act else None
+    ws, nws = _workspace(workspace, dev)
     _check(lib.ds4moe_grouped_matmul_backward(
-        ctypes.byref(m), rows, _operand("x", x, dt, dev), xr, _operand("w", w, dt, dev), _operand("z", z, dt, dev),
-        _operand("dy", dy, dt, dev), _operand("expert_offsets", expert_offsets, i32, dev),
-        _operand("sorted_pair", sorted_pair, i32, dev), top_k, _operand("dx", dx, dt, dev),
-        _operand("dw", dw, gd, dev), _operand("dbias", dbias, gd, dev), _operand("workspace", workspace, None, dev),
-        _ws(workspace), _s(stream, dev)))
+        ctypes.byref(m), rows, _matrix("x", x, dt, xr, k, ldx, dev), xr, _matrix("w", w, dt, wrows, k, ldw, dev),
+        _matrix("z", z, dt, rows, m.out_dim, m.ldz, dev), _matrix("dy", dy, dt, rows, oc, m.ldy, dev),
+        _vector("expert_offsets", expert_offsets, i32, m.groups + 1, dev),
+        _vector("sorted_pair", sorted_pair, i32, rows, dev), top_k, _matrix("dx", dx, dt, rows, k, ldx, dev),
+        _matrix("dw", dw, gd, wrows, k, ldw, dev), _vector("dbias", dbias, gd, wrows, dev), ws, nws, _s(stream, dev)))
 
 
 # ---- token sampling ------------------------------------------------------------
@@ -371,10 +418,10 @@ def sample(B, V, logits, u, token, temperature=None, top_k=None, top_p=None, min
         ld = logits.stride(0)
     if logits.get_device() != dev:
         raise Ds4MoeError(-1, f"logits on {logits.device}, not on the current HIP device {dev}")
+    ws, nws = _workspace(workspace, dev)
     _check(lib.ds4moe_sample(
         B, V, logits.data_ptr(), ld, dtype, _vector("temperature", temperature, f32, B, dev),
         _vector("top_k", top_k, i32, B, dev), _vector("top_p", top_p, f32, B, dev),
         _vector("min_p", min_p, f32, B, dev), _vector("u", u, f32, B, dev), _vector("token", token, i32, B, dev),
         _vector("prob", prob, f32, B, dev),
-        _operand("workspace", workspace, None, dev), _ws(workspace),
-        _s(stream, dev)))
+        ws, nws, _s(stream, dev)))

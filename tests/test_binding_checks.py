@@ -126,3 +126,72 @@ def test_product_types(lib, fn, names, groups, dtype, grad):
         for dt in (torch.int64, torch.float64, torch.float16, torch.int32, torch.float32, torch.bfloat16):
             if dt != t.dtype:
                 refused(lib, ARG, f"{n} is {dt}", call, m, rows, **dict(a, **{n: t.to(dt)}))
+
+
+@pytest.mark.parametrize("fn,names,groups", CALLS, ids=[c[0] for c in CALLS])
+@pytest.mark.parametrize("act", ["silu", "swiglu"])
+def test_product_sizes_and_strides(lib, fn, names, groups, act):
+    vectors = ("bias", "dbias", "expert_offsets", "sorted_pair")
+    for pad in (0, 8):
+        m, rows, a = product("bf16", "f32", act, groups, pad=pad)
+        call, a = getattr(ds4, fn), pick(a, names)
+        accepted(lib, call, m, rows, **a)
+        for n, t in a.items():
+            cols, last = t.shape[-1], t.dim() - 1
+            if n in vectors:
+                flat = t.flatten()
+                bad = [flat[:-1], flat[:1].expand(flat.numel()), torch.stack([flat, flat], 1)[:, 0]]
+                good = [flat, torch.cat([flat, flat])]
+            else:
+                r = t.numel() // cols
+                # a row or a column too few; a row stride that is not the descriptor's; columns apart
+                bad = [t.narrow(t.dim() - 2, 0, t.shape[-2] - 1), t.narrow(last, 0, cols - 1),
+                       torch.zeros(*t.shape[:-1], cols + 16, dtype=t.dtype)[..., :cols],
+                       torch.zeros(*t.shape, 2, dtype=t.dtype)[..., 0],
+                       torch.zeros((r - 1) * (cols + pad) + cols - 1, dtype=t.dtype)]
+                if t.dim() == 3 and groups:     # experts that do not follow one another at out_dim rows
+                    bad.append(torch.zeros(t.shape[0], t.shape[1] + 1, cols + pad, dtype=t.dtype)[:, :-1, :cols])
+                whole = torch.zeros(r, cols + pad, dtype=t.dtype)
+                good = [whole, whole[:, :cols], whole.flatten(), torch.zeros(r // 2, 2, cols + pad, dtype=t.dtype)]
+                if n != "x" or fn.startswith("linear"):     # (x's rows are part of the grouped calls)
+                    good.append(torch.zeros(r + 3, cols + pad, dtype=t.dtype))
+            kw = {"x_rows": rows} if groups else {}
+            for b in bad:
+                refused(lib, SHAPE, f"{n} of shape", call, m, rows, **dict(a, **{n: b}), **kw)
+            for b in good:
+                accepted(lib, call, m, rows, **dict(a, **{n: b}), **kw)
+
+
+def test_product_unread_operands(lib):
+    """x is read for dw only, w for dx only, z for an activation only: otherwise they may be anything."""
+    m, rows, a = product(act="none")
+    accepted(lib, ds4.linear_backward, m, rows, None, a["w"], a["dy"], z=torch.zeros(1), dx=a["dx"])
+    accepted(lib, ds4.linear_backward, m, rows, a["x"], None, a["dy"], dw=a["dw"])
+    accepted(lib, ds4.linear_backward, m, rows, torch.zeros(1), torch.zeros(1), a["dy"], dbias=a["dbias"])
+
+
+def test_product_row_counts(lib):
+    """x's rows: as many as x_rows says (default: all of its leading dimensions); one row has no stride."""
+    m, rows, a = product(groups=3)
+    call = lambda **kw: ds4.grouped_matmul(m, rows, **dict(pick(a, GROUPED), **kw))
+    refused(lib, SHAPE, "x of shape", call, x_rows=rows + 1)
+    seen = []
+    lib.__class__ = type("R", (Recorder,), {"__getattr__": lambda self, n: lambda *args: seen.append(args[3]) or 0})
+    call(x=torch.zeros(2, 5, 24, dtype=BF))
+    call(x=torch.zeros(4, 24, dtype=BF))
+    call(x=torch.zeros(24 * 7, dtype=BF), x_rows=7)
+    assert seen == [10, 4, 7]
+    lib.__class__ = Recorder
+    m, rows, a = product(rows=1)
+    accepted(lib, ds4.linear, m, 1, torch.zeros(3, 40, dtype=BF)[:1, :24], a["w"], a["y"])
+    accepted(lib, ds4.linear, m, 1, torch.zeros(24, dtype=BF), a["w"], torch.zeros(16, dtype=BF))
+
+
+def test_workspace_with_gaps(lib):
+    """Bytes between a workspace's elements (or the same ones counted again) are not scratch."""
+    m, rows, a = product()
+    for ws in (torch.zeros(64, 2, dtype=torch.uint8)[:, 0], torch.zeros(1, dtype=torch.uint8).expand(4096)):
+        refused(lib, SHAPE, "workspace", ds4.linear, m, rows, **pick(a, FORWARD), workspace=ws)
+        B, V, b = sample_args()
+        refused(lib, SHAPE, "workspace", ds4.sample, B, V, **b, workspace=ws)
+    accepted(lib, ds4.linear, m, rows, **pick(a, FORWARD), workspace=torch.zeros(8, 8))
