@@ -1,0 +1,86 @@
+"""ds4moe_sample on rows past 16384 tokens, which several workgroups share in
+four launches: masked, infinite and extreme rows, shares of a row without a
+live token, padded rows, and batches of one workgroup per row.  The definition
+and the tolerances are those of the short rows' tests."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+ds4 = pytest.importorskip("bit_routed_moe_amd")
+from test_gpu_sample import INF, check, normal  # noqa: E402
+
+V = 40001
+FILTERS = ({}, dict(k=10), dict(p=0.8), dict(q=0.02), dict(T=0.0), dict(T=0.8, k=50, p=0.9, q=0.01))
+
+
+def masked_rows(dtype):
+    """12 rows, of each of which 10 workgroups read about 4001 tokens."""
+    l = normal(12, V, 2.0, 31).to(dtype)
+    lowest = torch.finfo(dtype).min
+    l[0] = -INF
+    l[1] = float("nan")
+    l[2, 1:] = -INF
+    l[3, :-1] = float("nan")
+    l[4, ::2] = -INF
+    l[5, 5:] = lowest
+    l[6, [7, 12345, 39999]] = INF
+    l[7] = lowest
+    l[8, :21000] = -INF          # all that lives in one share of the row
+    l[8, 21040:] = float("nan")
+    l[9, :30000] = -INF          # infinities in one share, live tokens in others
+    l[9, 38000:38004] = INF
+    l[10, 100:] = -1e4           # a mask of a large finite value
+    l[11] = INF
+    return l
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_masks(dtype):
+    for i, kw in enumerate(FILTERS):
+        print(f"masks {dtype} {kw}", flush=True)
+        check(masked_rows(dtype), seed=40 + i, **kw)
+
+
+def test_extreme_parameters():
+    l = normal(5, V, 2.0, 32)
+    for i, kw in enumerate((
+            dict(T=1e-30), dict(T=torch.tensor([1e-44, 1e-10, 1e4, 1e30, INF])), dict(T=float("nan")),
+            dict(k=torch.tensor([-5, 2 ** 31 - 1, V, V - 1, 1])), dict(p=torch.tensor([-1.0, 0.0, 1e-30, 1.0, INF])),
+            dict(q=torch.tensor([-1.0, 1e-30, 1.0, INF, 0.5])), dict(u=0.0),
+            dict(u=torch.tensor([-3.0, 0.0, 2.0 ** -24, 1 - 2.0 ** -24, 2.0 ** -60])),
+            dict(k=7, u=torch.tensor([1.0, 1.5, INF, -1.0, -INF])))):
+        print(f"extreme {kw}", flush=True)
+        check(l, seed=50 + i, **kw)
+    check(l * 100, seed=60)
+    check(normal(3, V, 2.0, 33) * 1e30, seed=61)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("ld", [V, V + 7, V + 1000])
+def test_padded_rows(dtype, ld):
+    """Rows at any distance and alignment; what lies between them is not read as a logit."""
+    t = torch.full((6, ld), 1e4, dtype=dtype)
+    t[:, :V] = normal(6, V, 2.0, ld, dtype)
+    check(t[:, :V], k=30, p=0.9, seed=3)
+    check(t[:, :V], T=1.3, p=0.95, q=0.001, seed=4)
+
+
+@pytest.mark.parametrize("B,V", [(520, 16385), (700, 17003)])
+def test_one_workgroup_per_row(B, V):
+    g = torch.Generator().manual_seed(B)
+    l = normal(B, V, 2.5, B)
+    l[::7, : V // 2] = -INF
+    check(l, T=0.3 + torch.rand(B, generator=g), k=torch.randint(0, 200, (B,), generator=g),
+          p=0.4 + 0.7 * torch.rand(B, generator=g), q=0.05 * torch.rand(B, generator=g), seed=8)
+
+
+@pytest.mark.parametrize("value", [-1e4, float(torch.finfo(torch.float32).min), -INF], ids=["1e4", "lowest", "inf"])
+def test_flat_rows_under_a_mask(value):
+    """Crowded bins where a mask's value is finite: the range of nearly equal logits is narrowed."""
+    l = normal(4, V, 0.004, 34)
+    l[:, ::3] = value
+    check(l, seed=1)
+    check(l, p=0.6, seed=2)
+    check(l, k=20001, p=0.9, seed=3)
+    check(l, q=0.9951, seed=4)
