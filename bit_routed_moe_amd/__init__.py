@@ -289,11 +289,12 @@ def _rows_apart(shape, strides, rows, cols, ld):
         return False
     if len(shape) == 1:                      # memory without rows
         return shape[0] >= (rows - 1) * ld + cols
-    n = 1
-    for size, stride in zip(shape[-2::-1], strides[-2::-1]):
-        if n < rows and size != 1 and stride != n * ld:
+    n, i = 1, len(shape) - 2
+    while i >= 0 and n < rows:
+        if shape[i] != 1 and strides[i] != n * ld:
             return False
-        n *= size
+        n *= shape[i]
+        i -= 1
     return shape[-1] >= cols and n >= rows
 
 
@@ -306,10 +307,11 @@ def _matrix(name, t, dtype, rows, cols, ld, dev):
     if t.dtype != dtype and dtype is not None:   # (None: the library refuses the descriptor)
         raise Ds4MoeError(-1, f"{name} is {t.dtype}, not {dtype}")
     ld = ld or cols
-    # (the ordinary tensor first: this is host time of every call)
-    if not ((t.is_contiguous() and t.dim() > 1 and t.shape[-1] == ld >= cols and t.numel() >= rows * ld)
-            or _rows_apart(t.shape, t.stride(), rows, cols, ld)):
-        raise Ds4MoeError(-2, f"{name} of shape {tuple(t.shape)}, strides {t.stride()}: not {rows} rows of {cols} "
+    shape, strides = t.shape, t.stride()
+    # (two dimensions, the ordinary case, first: this is host time of every call)
+    if not ((len(shape) == 2 and strides[0] == ld and strides[1] == 1 and shape[0] >= rows and shape[1] >= cols)
+            or _rows_apart(shape, strides, rows, cols, ld)):
+        raise Ds4MoeError(-2, f"{name} of shape {tuple(shape)}, strides {strides}: not {rows} rows of {cols} "
                               f"elements, {ld} apart")
     if t.get_device() != dev:
         raise Ds4MoeError(-1, f"{name} on {t.device}, not on the current HIP device {dev}")
