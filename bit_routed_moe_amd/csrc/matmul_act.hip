@@ -8,6 +8,8 @@
 // column sums of unrounded dz stay in fp32 registers, are joined over the 8
 // row lanes in LDS and written as one partial per split, and a second launch
 // adds the partials in split order (no atomics: reproducible).
+// 3.0 TB/s at 4096 rows of 2048 columns with GELU (17 us, and 7 to add 128
+// partials on 8 workgroups), 2.6 at 8192 rows of 2 x 2048 with SwiGLU (64 us).
 #include "matmul.hpp"
 
 namespace ds4 {

@@ -11,9 +11,9 @@
 // the lines, took 136 us for one token's gate/up products instead of 80, and
 // non-temporal loads 98).  Weights go first into the matrix instruction
 // (v_mfma_f32_16x16x32_bf16), so a lane's results belong to one token.  The
-// waves' partial sums are joined in LDS in wave order.  4.3 TB/s on one
-// 7168 x 7168 product (24 us), 5.8 TB/s on one token's gate/up products of 8
-// experts (80 us), 6.3 TB/s on a 131072 x 7168 head (300 us).
+// waves' partial sums are joined in LDS in wave order.  5.0 TB/s on one
+// 7168 x 7168 product (20.4 us), 5.9 TB/s on one token's gate/up products of 8
+// experts (79.5 us), 6.2 TB/s on a 131072 x 7168 head (301 us).
 //
 // The rows' group is found from the offsets in the kernel (a plan launch would
 // cost more than the product): workgroup row p of the grid is sorted row p,
@@ -174,15 +174,22 @@ int mr_kw(int K) {
 
 }  // namespace
 
-// Products that take these kernels, measured against the tile kernels:
-//   dense, 7168 wide: 1 row of 131072 columns 300 us against 320, 8 rows a tie
-//     (323), 16 rows 369 against 320 (the rows' own reads from L2 grow to half
-//     the weights'); with fewer columns also 16 rows win (7168 columns 31.6
-//     against 35.0 us, the tiles being too few).
-//   grouped (256 experts, 4096 columns of 7168): 8 pairs 80 us against 119,
-//     64 pairs 552 against 597, 256 pairs 1527 against 1648, 512 pairs a tie;
-//     with several pairs per expert the tiles win (64 pairs of 16 experts 104
-//     against 95, 128 of 64 experts 504 against 575).
+// Products that take these kernels; "a / b": us here / with the tile kernels,
+// weights read from memory each time (K -> N at some rows).
+//   dense, up to 8 rows: 2048 -> 8192 10.9 / 16.0, 7168 -> 4096 14.8 / 16.8,
+//     7168 -> 131072 310 / 309; at worst 7168 -> 1024 13.7 / 11.2 and 4096 ->
+//     131072 200 / 175.
+//   dense, 16 rows (the rows' own reads from L2 grow to half the weights'):
+//     2048 -> 8192 12.3 / 16.1, 4096 -> 4096 11.7 / 13.5, 7168 -> 4096 17.0 /
+//     17.3, but past about 2^24 weights the tiles win: 4096 -> 8192 19.4 / 17.8,
+//     7168 -> 8192 30.8 / 26.1, 7168 -> 16384 57.5 / 44.9, and from 32768
+//     columns on, where the rule leaves it to them, 7168 -> 32768 91 / 79.  A
+//     rule on weights in place of columns would serve 9 to 16 rows better.
+//   grouped, 256 experts: 7168 -> 4096 8 pairs 80 / 84, 64 499 / 519, 256 1515
+//     / 1528; 2048 -> 1024 64 pairs 39 / 45, 256 125 / 124; 2048 -> 7168 64
+//     pairs 267 / 264, 256 828 / 775.  64 experts: 7168 -> 4096 64 pairs 399 /
+//     410, 128 505 / 500, 256 (tiles) 634 / 601.  8 experts: 7168 -> 4096 8
+//     pairs 58 / 64, 16 74 / 68, 32 (tiles) 95 / 84.
 bool mr_takes(int P, int N, int E) {
     if (E > 1) return P <= 16 || (P <= 256 && P <= 2 * E);
     return P <= 8 || (P <= 16 && N < 32768);

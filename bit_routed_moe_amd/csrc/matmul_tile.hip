@@ -26,8 +26,8 @@
 //     columns, and a lane gets its column's 4 values).
 // Counters: no LDS bank conflicts in any mode; at 256 x 256 matrix cores busy
 // 61% (forward), 49% (dgrad) and 46% (wgrad) of the cycles.  1.2 PFLOP/s at 4096
-// x 7168 -> 4096 with SwiGLU (203 us; the library's plain product 169), 1.06
-// over dx and dW of 4096 rows, 7168 -> 2048 (112 + 116 us).  Groups of few rows
+// x 7168 -> 4096 with SwiGLU (201 us; the library's plain product 169), 1.07
+// over dx and dW of 4096 rows, 7168 -> 2048 (109 + 115 us).  Groups of few rows
 // are bound by their weights (4096 tokens' down products of 256 experts at 4.1
 // TB/s), their dW by each tile's start and writing (25% busy).
 // The column operand goes first into the matrix instruction, so a lane holds 4
@@ -370,7 +370,8 @@ __global__ __launch_bounds__(64 * WR * WC) void mt_kernel(MmArgs a, int tr, int 
         __syncthreads();
     }
     // in stage st, behind its barrier: the half of the ring behind stage st has
-    // been read, and is needed again in 6 stages at the earliest
+    // been read; what it then holds, stage st + 8 on, is needed first by the
+    // DMAs that are issued up to ST stages ahead, so in 5 stages at the earliest
     auto refill = [&](int st) {
         if (MODE == MM_WGRAD && st % HALF == HALF / 2 && st / HALF > sb / HALF) fill_rows((st / HALF + 1) * HALF);
     };
@@ -563,11 +564,13 @@ __global__ __launch_bounds__(256) void mt_join_kernel(MmArgs a, int bm) {
 
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// Tile shapes, with what was measured of them over M = 24 .. 4096 rows of
-// 512 .. 8192 x 512 .. 8192 products, all three modes within 15% (us per stage
-// of 64 contraction columns): lat of a workgroup by itself on its CU, thr per
-// workgroup and CU when the chip is full; wgs that share a CU, so that one's
-// start and end hide behind another's stages.
+// Tile shapes, with the times that the estimate takes from measurement (us per
+// stage of 64 contraction columns): lat of a workgroup by itself on its CU, thr
+// per workgroup and CU when the chip is full; wgs that share a CU, so that one's
+// start and end hide behind another's stages.  Of 66 products (24 .. 16384 rows,
+// dense and of 8 .. 64 groups, 300 .. 8192 x 512 .. 8192, three modes), timed in
+// every shape and split, the choice is within 15% of the best in 65; the other
+// is 2048 rows of 8 groups, 1024 -> 1024, at 24.8 us against 19.0.
 struct MtShape {
     int br, bc;
     double lat, thr;

@@ -21,7 +21,15 @@
 // into the row's); the collection; the answer, one workgroup per row.  Where
 // more tokens than fit lie in the bins of a crossing (nearly flat rows, or
 // many equal logits) the last launch narrows each crossing down by itself,
-// pass by pass over the row.
+// pass by pass over the row: 64 rows of 131072 with top-p take 79 us where flat
+// rows fill fine bins, 381 us where a mask of -1e4 keeps the bins wide (42 us
+// and 346 us at one row), 1.1 ms where all logits are equal.
+//
+// 64 rows of 131072 are bound by waiting: vector units are busy for 53%, 40%,
+// 22% and 4% of the four launches, LDS for 12%, 21%, 9% and 3%; each workgroup
+// has its scans, searches and barriers once, however few tokens it reads.  256
+// rows of 50003 in bf16: 49%, 57%, 45% and 25%, LDS 8%, 37% (most of it
+// conflicts of the histogram's atomics), 10% and 22%.
 #include "common.hpp"
 #include "launch.hpp"
 
