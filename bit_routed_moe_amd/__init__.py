@@ -285,10 +285,10 @@ def _workspace(t, dev):
 def _rows_apart(shape, strides, rows, cols, ld):
     """Whether a tensor's first `rows` rows, counted over all its dimensions but
     the last, are `cols` or more elements that start `ld` apart."""
-    if not shape or (cols > 1 and strides[-1] != 1):
+    if not shape or 0 in shape or (cols > 1 and strides[-1] != 1):
         return False
     if len(shape) == 1:                      # memory without rows
-        return shape[0] >= (rows - 1) * ld + cols
+        return shape[0] >= (rows - 1) * ld + cols and (strides[0] == 1 or shape[0] == 1)
     n, i = 1, len(shape) - 2
     while i >= 0 and n < rows:
         if shape[i] != 1 and strides[i] != n * ld:
@@ -425,5 +425,4 @@ def sample(B, V, logits, u, token, temperature=None, top_k=None, top_p=None, min
         B, V, logits.data_ptr(), ld, dtype, _vector("temperature", temperature, f32, B, dev),
         _vector("top_k", top_k, i32, B, dev), _vector("top_p", top_p, f32, B, dev),
         _vector("min_p", min_p, f32, B, dev), _vector("u", u, f32, B, dev), _vector("token", token, i32, B, dev),
-        _vector("prob", prob, f32, B, dev),
-        ws, nws, _s(stream, dev)))
+        _vector("prob", prob, f32, B, dev), ws, nws, _s(stream, dev)))

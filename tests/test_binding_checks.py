@@ -195,3 +195,16 @@ def test_workspace_with_gaps(lib):
         B, V, b = sample_args()
         refused(lib, SHAPE, "workspace", ds4.sample, B, V, **b, workspace=ws)
     accepted(lib, ds4.linear, m, rows, **pick(a, FORWARD), workspace=torch.zeros(8, 8))
+
+
+def test_product_empty_and_strided_memory(lib):
+    """A tensor without elements has no row, and memory without rows has no gaps."""
+    m, _, a = product(rows=1)
+    w, y = a["w"], a["y"]
+    for bad in (torch.zeros(0, 24, dtype=BF), torch.zeros(0, 1, 24, dtype=BF), torch.zeros(1, 0, 24, dtype=BF)):
+        refused(lib, SHAPE, "x of shape", ds4.linear, m, 1, bad, w, y)
+    m = ds4.make_matmul(1, 16, ldx=8, ldw=8)
+    w = torch.zeros(16, 8, dtype=BF)[:, :1]
+    accepted(lib, ds4.linear, m, 2, torch.zeros(9, dtype=BF), w, torch.zeros(2, 16, dtype=BF))
+    accepted(lib, ds4.linear, m, 2, torch.zeros(2, 8, dtype=BF)[:, :1], w, torch.zeros(2, 16, dtype=BF))
+    refused(lib, SHAPE, "x of shape", ds4.linear, m, 2, torch.zeros(18, dtype=BF)[::2], w, torch.zeros(2, 16, dtype=BF))
