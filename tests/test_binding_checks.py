@@ -207,4 +207,5 @@ def test_product_empty_and_strided_memory(lib):
     w = torch.zeros(16, 8, dtype=BF)[:, :1]
     accepted(lib, ds4.linear, m, 2, torch.zeros(9, dtype=BF), w, torch.zeros(2, 16, dtype=BF))
     accepted(lib, ds4.linear, m, 2, torch.zeros(2, 8, dtype=BF)[:, :1], w, torch.zeros(2, 16, dtype=BF))
-    refused(lib, SHAPE, "x of shape", ds4.linear, m, 2, torch.zeros(18, dtype=BF)[::2], w, torch.zeros(2, 16, dtype=BF))
+    x = torch.zeros(18, dtype=BF)[::2]
+    refused(lib, SHAPE, "x of shape", ds4.linear, m, 2, x, w, torch.zeros(2, 16, dtype=BF))

@@ -170,3 +170,125 @@ def test_error_norms(rows, K, N, groups, gather_k, act, dtype, grad):
     norm_check("dx", p.dx[:end], torch.cat(dx), norm_limit(dtype, N, act, operand))
     norm_check("dw", p.dw, torch.stack(dw), norm_limit(grad, rows, act, operand))
     norm_check("dbias", p.dbias, torch.stack(db), norm_limit(grad, rows, act, 2.0 ** -16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,K,N", [(3, 1 << 20, 24), (20, 1 << 20, 8), (2, 16, 1 << 20), (20, 8, (1 << 20) - 8)])
+def test_largest_widths(rows, K, N, dtype):
+    print(f"largest {rows}x{K}->{N} {dtype}", flush=True)
+    run_both(Signs(rows, K, N, dtype, "none", bias=True, grad="f32", seed=7))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_most_rows(dtype):
+    """2^24 rows, made on the GPU: every sum over them stays below 2^24."""
+    rows, n = (1 << 24) - 5, 8
+    print(f"most rows {dtype}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    mk = lambda *s: (torch.randint(0, 2, s, generator=g, device=DEV, dtype=torch.int8) * 2 - 1).to(TD[dtype])
+    x, w, dy = mk(rows, n), mk(n, n), mk(rows, n)
+    y, dx = torch.empty_like(dy), torch.empty_like(x)
+    dw, db = torch.empty(n, n, device=DEV), torch.empty(n, device=DEV)
+    m = ds4.make_matmul(n, n, dtype=dtype, grad="f32")
+    ws = torch.empty(max(16, ds4.matmul_workspace_bytes(m, rows), ds4.matmul_workspace_bytes(m, rows, True)),
+                     dtype=torch.uint8, device=DEV)
+    ds4.linear(m, rows, x, w, y, workspace=ws)
+    ds4.linear_backward(m, rows, x, w, dy, dx=dx, dw=dw, dbias=db, workspace=ws)
+    assert torch.equal(y.float(), x.float() @ w.float().t()) and torch.equal(dx.float(), dy.float() @ w.float())
+    assert torch.equal(dw.double(), dy.double().t() @ x.double()) and torch.equal(db.double(), dy.double().sum(0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [3, 200, 5000])
+def test_1024_groups(rows, dtype):
+    """The most groups, most of them empty or of a few rows."""
+    g = torch.Generator().manual_seed(rows)
+    groups = torch.bincount(torch.randint(0, 1024, (rows,), generator=g) // 3 * 3, minlength=1024).tolist()
+    print(f"1024 groups, {rows} rows {dtype}", flush=True)
+    run_both(Signs(rows + 2, 72, 40, dtype, "none", groups=groups, gather_k=2, bias=True, grad="f32", seed=rows))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [12, 700])
+def test_nan_stays_in_its_rows_and_groups(rows, dtype):
+    """NaN and infinities in rows of no group, in rows of x that no row reads and in one expert's operands reach no
+    other result."""
+    groups = [rows // 4, 0, rows // 2, rows - rows // 4 - rows // 2]
+    p = Signs(rows + 3, 136, 72, dtype, "none", groups=groups, gather_k=2, bias=True, grad="f32", seed=rows)
+    a, b, own = p.off_h[2], p.off_h[3], p.x_rows - 1
+    src = p.src.clone()
+    src[(src == 0) | (src == own)] = 1      # token 0 is read by no row, the last one by one of the third expert's
+    src[a] = own
+    p.src = src
+    p.pairs.copy_((2 * src).to(torch.int32))
+    p.x[0] = float("nan")
+    p.dy[rows:] = float("inf")
+    p.x[own] = float("nan")
+    p.w[1] = float("inf")                   # an expert without rows
+    p.dy[a] = float("nan")
+    p.forward()
+    p.backward()
+    x, w = p.x.double()[p.src.to(DEV)], p.w.double()
+    for e in (0, 3):
+        i, j = p.off_h[e], p.off_h[e + 1]
+        p.same("y", p.y[i:j], x[i:j] @ w[e].t() + p.bias[e].double())
+        p.same("dx", p.dx[i:j], p.dy[i:j].double() @ w[e])
+        p.same("dw", p.dw[e], p.dy[i:j].double().t() @ x[i:j])
+        p.same("dbias", p.dbias[e], p.dy[i:j].double().sum(0))
+    assert (p.dw[1] == 0).all() and (p.dbias[1] == 0).all()
+    p.same("y", p.y[a + 1:b], x[a + 1:b] @ w[2].t() + p.bias[2].double())
+    p.same("dx", p.dx[a + 1:b], p.dy[a + 1:b].double() @ w[2])
+    for t in (p.y[a], p.dx[a], p.dw[2], p.dbias[2]):
+        assert torch.isnan(t).all()
+    assert torch.isnan(p.y[rows:]).all() and torch.isnan(p.dx[rows:]).all()   # (left as they were)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh", "swiglu"])
+def test_extreme_preactivations(act, rows, dtype):
+    """Activations and their derivatives where squares, exponentials and products leave fp32's range.  z is x itself
+    (w the unit matrix), and dbias of one row is dz, unrounded.
+
+    A value is off by 16 * 2^-24 of itself (EVAL), and where it falls as e^-t by 4 roundings of t, at most 88 before
+    fp32's range ends; a derivative, whose terms cancel, by EVAL * (1 + |z|)^2, |z| counted up to 10 (behind that it
+    is 0 or 1 to within e^-10 * 11).  Past t = 88.72 e^t leaves fp32's range and the value is 0, which is off by less
+    than 88.73 * 2^-128 < 2^-121."""
+    v = torch.tensor([0.0, 2e-38, 1e-4, 0.7, 2.0, 5.0, 9.5, 13.0, 20.0, 88.0, 90.0, 101.0, 1e4, 1e13, 1e20, 3e38])
+    v = torch.cat([v, -v])
+    n = len(v)
+    if act == "swiglu":                      # each as the gate, and as the other factor
+        q = torch.full((n,), 0.25)
+        v = torch.cat([v, q, q, v])          # (gates: v and 1/4, then their partners)
+    z = v.to(TD[dtype]).to(DEV)
+    N = z.numel()
+    oc = N // 2 if act == "swiglu" else N
+    m = ds4.make_matmul(N, N, dtype=dtype, act=act, grad="f32")
+    ws = torch.empty(max(16, ds4.matmul_workspace_bytes(m, rows), ds4.matmul_workspace_bytes(m, rows, True)),
+                     dtype=torch.uint8, device=DEV)
+    x = z.expand(rows, N).contiguous()
+    y = torch.empty(rows, oc, dtype=TD[dtype], device=DEV)
+    zs = torch.empty_like(x)
+    ds4.linear(m, rows, x, torch.eye(N, dtype=TD[dtype], device=DEV), y, z=zs, workspace=ws)
+    assert torch.equal(zs, x)
+    zd = z.double()[None].requires_grad_()
+    if act == "gelu_tanh":                   # 1 + tanh as 2 sigmoid: nothing cancels
+        want = zd * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (zd + 0.044715 * zd ** 3))
+    else:
+        want = act64(zd, act)
+    h = HALF[dtype]
+    err = (y.double() - want).abs()
+    bad = ~(err <= (EVAL + 88 * 2.0 ** -22 + h) * 1.01 * want.abs() + 2.0 ** -121)
+    assert not bad.any(), (act, z[:oc][bad[0]].tolist(), y[0][bad[0]].tolist())
+    dy = torch.full((1, oc), 0.5, dtype=TD[dtype], device=DEV)
+    dbias = torch.empty(N, device=DEV)
+    ds4.linear_backward(m, 1, None, None, dy, z=z[None].contiguous(), dbias=dbias, workspace=ws)
+    dz, = torch.autograd.grad(want, zd, dy.double())
+    a = zd.detach().abs().clamp(max=10)
+    scale = (1 + a) ** 2
+    if act == "swiglu":                      # the gate's derivative times u, and silu of the gate
+        g, u = zd.detach().chunk(2, 1)
+        scale = torch.cat([(1 + g.abs().clamp(max=10)) ** 2 * u.abs(), (g * torch.sigmoid(g)).abs()], 1)
+    err = (dbias.double()[None] - dz).abs()
+    bad = ~(err <= EVAL * 0.5 * scale + 2.0 ** -121)
+    assert not bad.any(), (act, z[bad[0]].tolist(), dbias[bad[0]].tolist(), dz[bad].tolist())
