@@ -84,3 +84,20 @@ def test_flat_rows_under_a_mask(value):
     check(l, p=0.6, seed=2)
     check(l, k=20001, p=0.9, seed=3)
     check(l, q=0.9951, seed=4)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_longest_rows(dtype):
+    """2^20 tokens, also with all weights equal (their sum is 2^63)."""
+    l = normal(3, 1 << 20, 2.0, 35, dtype)
+    check(l, T=torch.tensor([0.7, 1.0, 1.5]), k=torch.tensor([0, 50, 100000]), p=torch.tensor([0.9, 1.0, 0.7]),
+          seed=5)
+    check(l, T=INF, seed=6)
+    check(l, T=INF, k=700001, p=0.75, seed=7)
+
+
+def test_most_rows():
+    l = normal(32768, 33, 2.0, 36)
+    g = torch.Generator().manual_seed(9)
+    check(l, T=0.2 + torch.rand(32768, generator=g), k=torch.randint(0, 40, (32768,), generator=g),
+          p=0.3 + 0.8 * torch.rand(32768, generator=g), q=0.05 * torch.rand(32768, generator=g), seed=10)
