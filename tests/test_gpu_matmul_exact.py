@@ -292,3 +292,43 @@ def test_extreme_preactivations(act, rows, dtype):
     err = (dbias.double()[None] - dz).abs()
     bad = ~(err <= EVAL * 0.5 * scale + 2.0 ** -121)
     assert not bad.any(), (act, z[bad[0]].tolist(), dbias[bad[0]].tolist(), dz[bad].tolist())
+
+
+def test_two_graphs_share_a_workspace():
+    """A gathered product with its gradients (split contraction, refilled rings) and a dense one in two captured
+    graphs over one workspace, replayed in turn with new inputs and eager calls between."""
+    ps = [Signs(16390, 128, 128, "bf16", "relu", groups=[8192, 0, 8190], gather_k=2, bias=True, grad="f32", seed=3),
+          Signs(100, 8192, 130, "bf16", "none", bias=True, grad="f32", seed=4)]
+    n = max(ds4.matmul_workspace_bytes(p.m, p.rows, back) for p in ps for back in (False, True))
+    ws = torch.full((n,), 0xA5, dtype=torch.uint8, device=DEV)
+
+    def both(p):
+        p.forward(ws=ws)
+        p.backward(ws=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for p in ps:
+            both(p)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs = []
+    for p in ps:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            both(p)
+        graphs.append(g)
+    gen = torch.Generator().manual_seed(9)
+    for rep in range(6):
+        for p, g in zip(ps, graphs):
+            signs(p.x, gen)
+            signs(p.dy, gen)
+            for t in (p.y, p.z, p.dx, p.dw, p.dbias):
+                t.fill_(float("nan"))
+            ws.fill_(0x5A)
+            torch.randn(1000, device=DEV).sum().item()
+            g.replay()
+            torch.cuda.synchronize()
+            p.check_forward()
+            p.check_backward()

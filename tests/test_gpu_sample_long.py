@@ -8,7 +8,8 @@ import torch
 pytestmark = pytest.mark.gpu
 
 ds4 = pytest.importorskip("bit_routed_moe_amd")
-from test_gpu_sample import INF, check, normal  # noqa: E402
+from helpers import DEV  # noqa: E402
+from test_gpu_sample import INF, check, normal, reference  # noqa: E402
 
 V = 40001
 FILTERS = ({}, dict(k=10), dict(p=0.8), dict(q=0.02), dict(T=0.0), dict(T=0.8, k=50, p=0.9, q=0.01))
@@ -101,3 +102,42 @@ def test_most_rows():
     g = torch.Generator().manual_seed(9)
     check(l, T=0.2 + torch.rand(32768, generator=g), k=torch.randint(0, 40, (32768,), generator=g),
           p=0.3 + 0.8 * torch.rand(32768, generator=g), q=0.05 * torch.rand(32768, generator=g), seed=10)
+
+
+def test_graphs_of_both_forms_share_a_workspace():
+    """The one-launch and the four-launch form captured, replayed in turn over one workspace with new logits."""
+    g = torch.Generator().manual_seed(12)
+    cases = []
+    for B, n in ((5, 9001), (3, V)):
+        lg = torch.empty(B, n, device=DEV)
+        kw = dict(temperature=torch.full((B,), 0.8, device=DEV), top_p=torch.full((B,), 0.9, device=DEV))
+        cases.append((B, n, lg, torch.rand(B, generator=g).to(DEV), torch.empty(B, dtype=torch.int32, device=DEV), kw))
+    ws = torch.full((ds4.sample_workspace_bytes(3, V),), 0xA5, dtype=torch.uint8, device=DEV)
+    call = lambda c: ds4.sample(c[0], c[1], c[2], c[3], c[4], workspace=ws, **c[5])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for c in cases:
+            c[2].zero_()
+            call(c)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs = []
+    for c in cases:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(c)
+        graphs.append(graph)
+    for rep in range(6):
+        for c, graph in zip(cases, graphs):
+            l = normal(c[0], c[1], 2.0, 70 + rep)
+            c[2].copy_(l)
+            c[4].fill_(-9)
+            ws.fill_(0x5A)
+            torch.randn(1000, device=DEV).sum().item()
+            graph.replay()
+            torch.cuda.synchronize()
+            host, u = l.double().numpy(), c[3].cpu()
+            T, p = float(torch.tensor(0.8)), float(torch.tensor(0.9))
+            for r in range(c[0]):
+                assert int(c[4][r]) == reference(host[r], T, 0, p, 0.0, float(u[r]))[0], (rep, r)
