@@ -19,6 +19,7 @@ __all__ = [
     "EXPORTS", "STAGE", "set_stage_events",
     "ACT", "Matmul", "make_matmul", "matmul_workspace_bytes", "linear", "linear_backward", "grouped_matmul",
     "grouped_matmul_backward", "sample", "sample_workspace_bytes",
+    "Rows", "make_rows", "dispatch", "dispatch_backward", "collect", "collect_backward", "route_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libds4moe.so")
@@ -36,6 +37,8 @@ EXPORTS = (
     "ds4moe_workspace_region", "ds4moe_forward_noalloc", "ds4moe_forward_noalloc_max_bytes",
     "ds4moe_linear", "ds4moe_linear_backward", "ds4moe_grouped_matmul", "ds4moe_grouped_matmul_backward",
     "ds4moe_matmul_workspace_bytes", "ds4moe_sample", "ds4moe_sample_workspace_bytes",
+    "ds4moe_dispatch", "ds4moe_dispatch_backward", "ds4moe_collect", "ds4moe_collect_backward",
+    "ds4moe_route_backward",
 )
 
 WS_REGION = {"topk_idx": 0, "topk_w": 1, "offsets": 2, "sorted_pair": 3, "pair_pos": 4, "active": 5,
@@ -59,6 +62,11 @@ class Matmul(ctypes.Structure):
                 [(n, ctypes.c_int64) for n in ("ldx", "ldw", "ldy", "ldz")])
 
 
+class Rows(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("hidden", "top_k", "dtype")] +
+                [(n, ctypes.c_int64) for n in ("ldx", "ldr")])
+
+
 class Ds4MoeError(RuntimeError):
     def __init__(self, status, message):
         super().__init__(f"ds4moe status {status}: {message}")
@@ -76,7 +84,7 @@ def _load():
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     cfgp, wp = ctypes.POINTER(Config), ctypes.POINTER(Weights)
-    mmp = ctypes.POINTER(Matmul)
+    mmp, rwp = ctypes.POINTER(Matmul), ctypes.POINTER(Rows)
     sigs = {
         "ds4moe_router_logits": (i32, [cfgp, i32, vp, vp, vp, vp]),
         "ds4moe_route": (i32, [cfgp, i32, vp, vp, vp, vp]),
@@ -102,6 +110,11 @@ def _load():
         "ds4moe_matmul_workspace_bytes": (sz, [mmp, i32, i32]),
         "ds4moe_sample": (i32, [i32, i32, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "ds4moe_sample_workspace_bytes": (sz, [i32, i32]),
+        "ds4moe_dispatch": (i32, [rwp, i32, i32, vp, vp, vp, vp, vp, vp]),
+        "ds4moe_collect": (i32, [rwp, i32, i32, vp, vp, vp, vp, vp, vp]),
+        "ds4moe_dispatch_backward": (i32, [rwp, i32, i32, vp, vp, vp, vp, vp, vp, vp]),
+        "ds4moe_collect_backward": (i32, [rwp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "ds4moe_route_backward": (i32, [cfgp, i32, vp, vp, vp, vp, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -394,6 +407,80 @@ def grouped_matmul_backward(m, rows, x, w, expert_offsets, dy, z=None, sorted_pa
         _vector("expert_offsets", expert_offsets, i32, m.groups + 1, dev),
         _vector("sorted_pair", sorted_pair, i32, rows, dev), top_k, _matrix("dx", dx, dt, rows, k, ldx, dev),
         _matrix("dw", dw, gd, wrows, k, ldw, dev), _vector("dbias", dbias, gd, wrows, dev), ws, nws, _s(stream, dev)))
+
+
+# ---- rows by expert and back ---------------------------------------------------
+
+def make_rows(hidden, top_k, dtype="bf16", ldx=0, ldr=0) -> Rows:
+    """Descriptor of rows that move between the tokens' and the experts' order:
+    row strides in elements of the tokens' tensors (ldx) and of those by expert
+    (ldr), 0: no gaps."""
+    return Rows(hidden, top_k, DTYPE[dtype], ldx, ldr)
+
+
+def _rows_plan(d, T):
+    """Type of a descriptor's rows, fp32, int32, pairs, and the current device."""
+    import torch
+    return ((torch.float32, torch.bfloat16)[d.dtype] if 0 <= d.dtype <= 1 else None, torch.float32, torch.int32,
+            T * d.top_k, _here())
+
+
+def dispatch(d, T, rows, x, pair_pos, out, topk_w=None, sorted_pair=None, stream=None):
+    """out[pair_pos[t, j]] = topk_w[t, j] * x[t] (weight 1 without topk_w); pairs
+    whose position is outside [0, rows) are dropped.  With sorted_pair, rows
+    whose entry is no pair are set to zero."""
+    dt, f32, i32, n, dev = _rows_plan(d, T)
+    _check(lib.ds4moe_dispatch(
+        ctypes.byref(d), T, rows, _matrix("x", x, dt, T, d.hidden, d.ldx, dev),
+        _vector("pair_pos", pair_pos, i32, n, dev), _vector("topk_w", topk_w, f32, n, dev),
+        _vector("sorted_pair", sorted_pair, i32, rows, dev), _matrix("out", out, dt, rows, d.hidden, d.ldr, dev),
+        _s(stream, dev)))
+
+
+def collect(d, T, rows, expert_rows, pair_pos, y, topk_w=None, base=None, stream=None):
+    """y[t] = base[t] + sum_j topk_w[t, j] * expert_rows[pair_pos[t, j]]."""
+    dt, f32, i32, n, dev = _rows_plan(d, T)
+    _check(lib.ds4moe_collect(
+        ctypes.byref(d), T, rows, _matrix("expert_rows", expert_rows, dt, rows, d.hidden, d.ldr, dev),
+        _vector("pair_pos", pair_pos, i32, n, dev), _vector("topk_w", topk_w, f32, n, dev),
+        _matrix("base", base, dt, T, d.hidden, d.ldx, dev), _matrix("y", y, dt, T, d.hidden, d.ldx, dev),
+        _s(stream, dev)))
+
+
+def dispatch_backward(d, T, rows, dout, pair_pos, topk_w=None, x=None, dx=None, dtopk_w=None, stream=None):
+    """Gradients of dispatch: dx, dtopk_w, or both (x is read for dtopk_w only)."""
+    dt, f32, i32, n, dev = _rows_plan(d, T)
+    x = None if dtopk_w is None else x
+    _check(lib.ds4moe_dispatch_backward(
+        ctypes.byref(d), T, rows, _matrix("x", x, dt, T, d.hidden, d.ldx, dev),
+        _matrix("dout", dout, dt, rows, d.hidden, d.ldr, dev), _vector("pair_pos", pair_pos, i32, n, dev),
+        _vector("topk_w", topk_w, f32, n, dev), _matrix("dx", dx, dt, T, d.hidden, d.ldx, dev),
+        _vector("dtopk_w", dtopk_w, f32, n, dev), _s(stream, dev)))
+
+
+def collect_backward(d, T, rows, dy, pair_pos, expert_rows=None, topk_w=None, sorted_pair=None, drows=None,
+                     dtopk_w=None, stream=None):
+    """Gradients of collect: drows, dtopk_w, or both (expert_rows is read for
+    dtopk_w only); sorted_pair as in dispatch."""
+    dt, f32, i32, n, dev = _rows_plan(d, T)
+    expert_rows = None if dtopk_w is None else expert_rows
+    _check(lib.ds4moe_collect_backward(
+        ctypes.byref(d), T, rows, _matrix("expert_rows", expert_rows, dt, rows, d.hidden, d.ldr, dev),
+        _matrix("dy", dy, dt, T, d.hidden, d.ldx, dev), _vector("pair_pos", pair_pos, i32, n, dev),
+        _vector("topk_w", topk_w, f32, n, dev), _vector("sorted_pair", sorted_pair, i32, rows, dev),
+        _matrix("drows", drows, dt, rows, d.hidden, d.ldr, dev), _vector("dtopk_w", dtopk_w, f32, n, dev),
+        _s(stream, dev)))
+
+
+def route_backward(cfg, T, topk_idx, topk_w, dtopk_w, dlogits, stream=None):
+    """dlogits [T, n_experts] of route from the gradient of its weights."""
+    import torch
+    f32, dev = torch.float32, _here()
+    n = T * cfg.top_k
+    _check(lib.ds4moe_route_backward(
+        ctypes.byref(cfg), T, _vector("topk_idx", topk_idx, torch.int32, n, dev),
+        _vector("topk_w", topk_w, f32, n, dev), _vector("dtopk_w", dtopk_w, f32, n, dev),
+        _vector("dlogits", dlogits, f32, T * cfg.n_experts, dev), _s(stream, dev)))
 
 
 # ---- token sampling ------------------------------------------------------------

@@ -316,6 +316,29 @@ int check_ld(const char* name, int64_t ld, int64_t cols, int64_t q) {
     return DS4MOE_OK;
 }
 
+// A descriptor of rows, and the strides of the tensors present.
+int check_rows(const ds4moe_rows* d, int32_t T, int32_t rows, bool has_x, bool has_r, ds4::TokenArgs& a) {
+    if (!d) return fail(DS4MOE_E_ARG, "d is NULL");
+    if (d->dtype != DS4MOE_DT_F32 && d->dtype != DS4MOE_DT_BF16) {
+        if (d->dtype == DS4MOE_DT_FP8_E4M3) return fail(DS4MOE_E_UNSUPPORTED, "fp8 rows");
+        return fail(DS4MOE_E_ARG, "dtype %d", d->dtype);
+    }
+    if (d->hidden < 1 || d->hidden > (1 << 20)) return fail(DS4MOE_E_SHAPE, "hidden %d not in [1, 2^20]", d->hidden);
+    if (d->top_k < 1 || d->top_k > 64) return fail(DS4MOE_E_SHAPE, "top_k %d not in [1, 64]", d->top_k);
+    if (T < 1 || T > (1 << 20)) return fail(DS4MOE_E_SHAPE, "T %d not in [1, 2^20]", T);
+    if (rows < 1) return fail(DS4MOE_E_SHAPE, "rows %d", rows);
+    const int64_t q = d->dtype == DS4MOE_DT_F32 ? 4 : 8;
+    a.H = d->hidden;
+    a.k = d->top_k;
+    a.T = T;
+    a.rows = rows;
+    a.ldx = d->ldx ? d->ldx : d->hidden;
+    a.ldr = d->ldr ? d->ldr : d->hidden;
+    if (has_x) TRY(check_ld("ldx", a.ldx, d->hidden, q));
+    if (has_r) TRY(check_ld("ldr", a.ldr, d->hidden, q));
+    return DS4MOE_OK;
+}
+
 // Validates a descriptor (strides aside, which depend on the tensors present).
 int check_mm(const ds4moe_matmul* m, int32_t rows) {
     if (!m) return fail(DS4MOE_E_ARG, "m is NULL");
@@ -769,6 +792,100 @@ int ds4moe_dequantize(int32_t wfmt, const void* data, const void* scales, int64_
                                              static_cast<const uint8_t*>(scales), n, out_f32, out_bf16,
                                              static_cast<hipStream_t>(stream)),
                       "dequantize");
+}
+
+int ds4moe_dispatch(const ds4moe_rows* d, int32_t T, int32_t rows, const void* x, const int32_t* pair_pos,
+                    const float* topk_w, const int32_t* sorted_pair, void* out, void* stream) {
+    ds4::TokenArgs a{};
+    TRY(check_rows(d, T, rows, true, true, a));
+    REQ_PTR(x);
+    REQ_PTR(pair_pos);
+    OPT_PTR(topk_w);
+    OPT_PTR(sorted_pair);
+    REQ_PTR(out);
+    a.src = x;
+    a.pair_pos = pair_pos;
+    a.topk_w = topk_w;
+    a.sorted_pair = sorted_pair;
+    a.out = out;
+    return hip_status(ds4::launch_tokens_to_rows(a, d->dtype == DS4MOE_DT_F32, static_cast<hipStream_t>(stream)),
+                      "dispatch");
+}
+
+int ds4moe_collect(const ds4moe_rows* d, int32_t T, int32_t rows, const void* expert_rows, const int32_t* pair_pos,
+                   const float* topk_w, const void* base, void* y, void* stream) {
+    ds4::TokenArgs a{};
+    TRY(check_rows(d, T, rows, true, true, a));
+    REQ_PTR(expert_rows);
+    REQ_PTR(pair_pos);
+    OPT_PTR(topk_w);
+    OPT_PTR(base);
+    REQ_PTR(y);
+    a.src = expert_rows;
+    a.pair_pos = pair_pos;
+    a.topk_w = topk_w;
+    a.base = base;
+    a.out = y;
+    return hip_status(ds4::launch_rows_to_tokens(a, d->dtype == DS4MOE_DT_F32, static_cast<hipStream_t>(stream)),
+                      "collect");
+}
+
+int ds4moe_dispatch_backward(const ds4moe_rows* d, int32_t T, int32_t rows, const void* x, const void* dout,
+                             const int32_t* pair_pos, const float* topk_w, void* dx, float* dtopk_w, void* stream) {
+    ds4::TokenArgs a{};
+    TRY(check_rows(d, T, rows, true, true, a));
+    if (!dx && !dtopk_w) return fail(DS4MOE_E_ARG, "dx and dtopk_w are both NULL");
+    if (dtopk_w) REQ_PTR(x);
+    REQ_PTR(dout);
+    REQ_PTR(pair_pos);
+    OPT_PTR(topk_w);
+    OPT_PTR(dx);
+    OPT_PTR(dtopk_w);
+    a.src = dout;
+    a.pair_pos = pair_pos;
+    a.topk_w = topk_w;
+    a.out = dx;
+    a.theirs = x;
+    a.dw = dtopk_w;
+    return hip_status(ds4::launch_rows_to_tokens(a, d->dtype == DS4MOE_DT_F32, static_cast<hipStream_t>(stream)),
+                      "dispatch backward");
+}
+
+int ds4moe_collect_backward(const ds4moe_rows* d, int32_t T, int32_t rows, const void* expert_rows, const void* dy,
+                            const int32_t* pair_pos, const float* topk_w, const int32_t* sorted_pair, void* drows,
+                            float* dtopk_w, void* stream) {
+    ds4::TokenArgs a{};
+    TRY(check_rows(d, T, rows, true, true, a));
+    if (!drows && !dtopk_w) return fail(DS4MOE_E_ARG, "drows and dtopk_w are both NULL");
+    if (dtopk_w) REQ_PTR(expert_rows);
+    REQ_PTR(dy);
+    REQ_PTR(pair_pos);
+    OPT_PTR(topk_w);
+    OPT_PTR(sorted_pair);
+    OPT_PTR(drows);
+    OPT_PTR(dtopk_w);
+    a.src = dy;
+    a.pair_pos = pair_pos;
+    a.topk_w = topk_w;
+    a.sorted_pair = sorted_pair;
+    a.out = drows;
+    a.theirs = expert_rows;
+    a.dw = dtopk_w;
+    return hip_status(ds4::launch_tokens_to_rows(a, d->dtype == DS4MOE_DT_F32, static_cast<hipStream_t>(stream)),
+                      "collect backward");
+}
+
+int ds4moe_route_backward(const ds4moe_config* cfg, int32_t T, const int32_t* topk_idx, const float* topk_w,
+                          const float* dtopk_w, float* dlogits, void* stream) {
+    TRY(check_cfg(cfg));
+    TRY(check_T(cfg, T));
+    REQ_PTR(topk_idx);
+    REQ_PTR(topk_w);
+    REQ_PTR(dtopk_w);
+    REQ_PTR(dlogits);
+    return hip_status(ds4::launch_route_backward(T, cfg->n_experts, cfg->top_k, topk_idx, topk_w, dtopk_w, dlogits,
+                                                 static_cast<hipStream_t>(stream)),
+                      "route backward");
 }
 
 size_t ds4moe_matmul_workspace_bytes(const ds4moe_matmul* m, int32_t rows, int32_t backward) {

@@ -187,4 +187,23 @@ hipError_t launch_sample(int B, int V, int64_t ld, bool f32, const void* logits,
                          float* prob, void* workspace, hipStream_t s);
 size_t sample_workspace_bytes(int B, int V);
 
+// Rows between the tokens' order ([T][ldx]) and the experts' order
+// ([rows][ldr]) (tokens.hip has the formulas).
+struct TokenArgs {
+    int H, k, T, rows;
+    int64_t ldx, ldr;
+    const int32_t* pair_pos;      // [T*k]
+    const int32_t* sorted_pair;   // [rows], null: no rows to clear
+    const float* topk_w;          // [T*k], null: 1
+    const void* src;              // to rows: [T][ldx]; to tokens: [rows][ldr]
+    const void* base;             // to tokens: [T][ldx] or null
+    void* out;                    // to rows: [rows][ldr]; to tokens: [T][ldx]; null: weights' gradients alone
+    const void* theirs;           // with dw: to rows [rows][ldr], to tokens [T][ldx]
+    float* dw;                    // [T*k] or null
+};
+hipError_t launch_tokens_to_rows(const TokenArgs& a, bool f32, hipStream_t s);
+hipError_t launch_rows_to_tokens(const TokenArgs& a, bool f32, hipStream_t s);
+hipError_t launch_route_backward(int T, int E, int k, const int32_t* idx, const float* w, const float* dw,
+                                 float* dlogits, hipStream_t s);
+
 }  // namespace ds4

@@ -290,6 +290,65 @@ int ds4moe_dequantize(int32_t wfmt, const void* data, const void* scales, int64_
 int ds4moe_quantize_mxfp8(const void* x_bf16, int64_t n, uint8_t* codes, uint8_t* scales,
                           void* stream);
 
+/* ---- rows by expert and back ----------------------------------------------
+ * Copies of the tokens' rows laid out by expert (dispatch), the experts' rows
+ * summed back at their tokens (collect), with the router's weights applied on
+ * either way, and the gradients.  ds4moe_grouped_matmul takes the rows in
+ * between.  For token t, slot j, with pos = pair_pos[t * top_k + j] and w =
+ * topk_w[t * top_k + j] (1 where topk_w is NULL):
+ *   dispatch           out[pos] = w * x[t]
+ *   dispatch_backward  dx[t] = sum_j w * dout[pos];  dtopk_w[t][j] = sum_h x[t][h] * dout[pos][h]
+ *   collect            y[t] = base[t] + sum_j w * expert_rows[pos]
+ *   collect_backward   drows[pos] = w * dy[t];       dtopk_w[t][j] = sum_h expert_rows[pos][h] * dy[t][h]
+ *                      (base's gradient is dy itself)
+ * pair_pos int32 [T*top_k] is ds4moe_permute's, or of any other layout of
+ * `rows` rows, such as a fixed number of rows for each expert.  A pair whose
+ * position is outside [0, rows) is dropped: it adds nothing and its weight's
+ * gradient is 0.  Rows that no pair names are left as they were; with
+ * sorted_pair (int32 [rows], the pair of each row) dispatch and
+ * collect_backward write zeros to the rows whose entry is outside
+ * [0, T*top_k).  Positions have to differ: where two pairs name one row, which
+ * of the two it receives is undefined.
+ * ds4moe_combine is collect for a layer's own widths; the pages do not show
+ * these steps (their engine's expert kernels are not shown).
+ * Rows have `hidden` columns of dtype (F32 or BF16), any number from 1 to
+ * 2^20; ldx (x, dx, base, y, dy) and ldr (out, dout, expert_rows, drows) are
+ * row strides in elements, 0 = no gaps, under the rules of the products'
+ * strides below.  Products and sums are fp32 (slots in order), results are
+ * rounded once; topk_w and dtopk_w are fp32.
+ * 1 <= top_k <= 64, 1 <= T <= 2^20, T * top_k < 2^31, rows >= 1.  Outputs must
+ * not overlap inputs, except that y may be base itself and drows may be
+ * expert_rows itself. */
+typedef struct {
+    int32_t hidden, top_k, dtype;
+    int64_t ldx, ldr;
+} ds4moe_rows;
+
+int ds4moe_dispatch(const ds4moe_rows* d, int32_t T, int32_t rows, const void* x, const int32_t* pair_pos,
+                    const float* topk_w, const int32_t* sorted_pair, void* out, void* stream);
+int ds4moe_collect(const ds4moe_rows* d, int32_t T, int32_t rows, const void* expert_rows, const int32_t* pair_pos,
+                   const float* topk_w, const void* base, void* y, void* stream);
+
+/* dx and dtopk_w may each be NULL (not computed; not both); x is read for
+ * dtopk_w only (NULL otherwise allowed). */
+int ds4moe_dispatch_backward(const ds4moe_rows* d, int32_t T, int32_t rows, const void* x, const void* dout,
+                             const int32_t* pair_pos, const float* topk_w, void* dx, float* dtopk_w, void* stream);
+/* drows and dtopk_w may each be NULL (not both); expert_rows is read for
+ * dtopk_w only. */
+int ds4moe_collect_backward(const ds4moe_rows* d, int32_t T, int32_t rows, const void* expert_rows, const void* dy,
+                            const int32_t* pair_pos, const float* topk_w, const int32_t* sorted_pair, void* drows,
+                            float* dtopk_w, void* stream);
+
+/* Gradient of ds4moe_route's weights with respect to its logits: with w =
+ * topk_w[t] and dw = dtopk_w[t], dlogits[t][topk_idx[t][j]] = w_j * (dw_j -
+ * sum_i w_i dw_i) for the chosen experts, 0 for the others (the choice itself
+ * has no gradient).  topk_idx holds distinct ids within a token (as route
+ * makes; ids outside [0, n_experts) are skipped).  dlogits: fp32
+ * [T][n_experts], every element written.  Of cfg, n_experts and top_k are
+ * used; the other fields must be valid. */
+int ds4moe_route_backward(const ds4moe_config* cfg, int32_t T, const int32_t* topk_idx, const float* topk_w,
+                          const float* dtopk_w, float* dlogits, void* stream);
+
 /* ---- products at original precision ---------------------------------------
  * Matrix products of rows with bf16 or fp32 weights, dense (ds4moe_linear) or
  * grouped by expert with ragged sizes (ds4moe_grouped_matmul), with their
