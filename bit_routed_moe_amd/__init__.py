@@ -20,6 +20,7 @@ __all__ = [
     "ACT", "Matmul", "make_matmul", "matmul_workspace_bytes", "linear", "linear_backward", "grouped_matmul",
     "grouped_matmul_backward", "sample", "sample_workspace_bytes",
     "Rows", "make_rows", "dispatch", "dispatch_backward", "collect", "collect_backward", "route_backward",
+    "LogitRules", "adjust_logits",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libds4moe.so")
@@ -38,7 +39,7 @@ EXPORTS = (
     "ds4moe_linear", "ds4moe_linear_backward", "ds4moe_grouped_matmul", "ds4moe_grouped_matmul_backward",
     "ds4moe_matmul_workspace_bytes", "ds4moe_sample", "ds4moe_sample_workspace_bytes",
     "ds4moe_dispatch", "ds4moe_dispatch_backward", "ds4moe_collect", "ds4moe_collect_backward",
-    "ds4moe_route_backward",
+    "ds4moe_route_backward", "ds4moe_adjust_logits",
 )
 
 WS_REGION = {"topk_idx": 0, "topk_w": 1, "offsets": 2, "sorted_pair": 3, "pair_pos": 4, "active": 5,
@@ -65,6 +66,13 @@ class Matmul(ctypes.Structure):
 class Rows(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("hidden", "top_k", "dtype")] +
                 [(n, ctypes.c_int64) for n in ("ldx", "ldr")])
+
+
+class LogitRules(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in (
+        "history", "history_offsets", "prompt_len", "repetition", "presence", "frequency", "bias_token", "bias_value",
+        "bias_offsets", "mask", "mask_row")] +
+        [("mask_ld", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("n_history", "n_bias", "mask_rows")])
 
 
 class Ds4MoeError(RuntimeError):
@@ -114,6 +122,7 @@ def _load():
         "ds4moe_collect": (i32, [rwp, i32, i32, vp, vp, vp, vp, vp, vp]),
         "ds4moe_dispatch_backward": (i32, [rwp, i32, i32, vp, vp, vp, vp, vp, vp, vp]),
         "ds4moe_collect_backward": (i32, [rwp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "ds4moe_adjust_logits": (i32, [i32, i32, vp, i64, i32, ctypes.POINTER(LogitRules), vp, i64, i32, vp]),
         "ds4moe_route_backward": (i32, [cfgp, i32, vp, vp, vp, vp, vp]),
     }
     for name, (res, args) in sigs.items():
@@ -481,6 +490,59 @@ def route_backward(cfg, T, topk_idx, topk_w, dtopk_w, dlogits, stream=None):
         ctypes.byref(cfg), T, _vector("topk_idx", topk_idx, torch.int32, n, dev),
         _vector("topk_w", topk_w, f32, n, dev), _vector("dtopk_w", dtopk_w, f32, n, dev),
         _vector("dlogits", dlogits, f32, T * cfg.n_experts, dev), _s(stream, dev)))
+
+
+# ---- rules on logits -----------------------------------------------------------
+
+def _logit_rows(name, t, B, V, dev):
+    """Type, row stride and device pointer of B rows of V logits."""
+    import torch
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise Ds4MoeError(-1, f"{name} is {t.dtype}, not torch.float32 or torch.bfloat16")
+    rows = 1 if t.dim() < 2 else t.shape[0]
+    if t.dim() not in (1, 2) or rows < B or t.shape[-1] < V or (V > 1 and t.stride(-1) != 1):
+        raise Ds4MoeError(-2, f"{name} of shape {tuple(t.shape)}, strides {t.stride()} for {B} rows of {V}")
+    if t.get_device() != dev:
+        raise Ds4MoeError(-1, f"{name} on {t.device}, not on the current HIP device {dev}")
+    return int(t.dtype == torch.bfloat16), t.stride(0) if B > 1 else V, t.data_ptr()
+
+
+def adjust_logits(B, V, logits, out, history=None, history_offsets=None, prompt_len=None, repetition=None,
+                  presence=None, frequency=None, bias_token=None, bias_value=None, bias_offsets=None, mask=None,
+                  mask_row=None, stream=None):
+    """out [B][V] = logits [B][V] (fp32 or bf16 each; out may be logits) under
+    penalties for the tokens of each row's history, biases and a mask; None
+    switches a rule off.  history, history_offsets [B + 1], prompt_len [B],
+    bias_token, bias_offsets [B + 1], mask [rows][words] and mask_row [B] are
+    int32, the others fp32 (repetition, presence, frequency [B], bias_value as
+    long as bias_token), all contiguous but for the rows of logits, out and
+    mask."""
+    import torch
+    f32, i32, dev = torch.float32, torch.int32, _here()
+    dt, ld, src = _logit_rows("logits", logits, B, V, dev)
+    odt, ldo, dst = _logit_rows("out", out, B, V, dev)
+    nh = 0 if history is None else history.numel()
+    nb = 0 if bias_token is None else bias_token.numel()
+    # (an empty list is a list all the same; it need not have memory)
+    r = LogitRules(
+        _vector("history", history, i32, nh, dev), _vector("history_offsets", history_offsets, i32, B + 1, dev),
+        _vector("prompt_len", prompt_len, i32, B, dev), _vector("repetition", repetition, f32, B, dev),
+        _vector("presence", presence, f32, B, dev), _vector("frequency", frequency, f32, B, dev),
+        _vector("bias_token", bias_token, i32, nb, dev), _vector("bias_value", bias_value, f32, nb, dev),
+        _vector("bias_offsets", bias_offsets, i32, B + 1, dev), None, _vector("mask_row", mask_row, i32, B, dev), 0,
+        nh, nb, 0)
+    if mask is not None:
+        words = (V + 31) // 32
+        if mask.dtype != i32:
+            raise Ds4MoeError(-1, f"mask is {mask.dtype}, not {i32}")
+        if (mask.dim() != 2 or mask.shape[1] < words or (words > 1 and mask.stride(1) != 1) or
+                (mask.shape[0] > 1 and mask.stride(0) < words)):
+            raise Ds4MoeError(-2, f"mask of shape {tuple(mask.shape)}, strides {mask.stride()} for {V} tokens")
+        if mask.get_device() != dev:
+            raise Ds4MoeError(-1, f"mask on {mask.device}, not on the current HIP device {dev}")
+        r.mask, r.mask_rows = mask.data_ptr(), mask.shape[0]
+        r.mask_ld = mask.stride(0) if mask.shape[0] > 1 else words
+    _check(lib.ds4moe_adjust_logits(B, V, src, ld, dt, ctypes.byref(r), dst, ldo, odt, _s(stream, dev)))
 
 
 # ---- token sampling ------------------------------------------------------------

@@ -1000,4 +1000,77 @@ int ds4moe_sample(int32_t B, int32_t V, const void* logits, int64_t ld, int32_t 
                       "sample");
 }
 
+int ds4moe_adjust_logits(int32_t B, int32_t V, const void* logits, int64_t ld, int32_t dtype,
+                         const ds4moe_logit_rules* rules, void* out, int64_t ld_out, int32_t out_dtype, void* stream) {
+    for (const int32_t t : {dtype, out_dtype}) {
+        if (t == DS4MOE_DT_FP8_E4M3) return fail(DS4MOE_E_UNSUPPORTED, "fp8 logits");
+        if (t != DS4MOE_DT_F32 && t != DS4MOE_DT_BF16) return fail(DS4MOE_E_ARG, "dtype %d", t);
+    }
+    if (B < 1 || B > 32768) return fail(DS4MOE_E_SHAPE, "B %d not in [1, 32768]", B);
+    if (V < 1 || V > (1 << 20)) return fail(DS4MOE_E_SHAPE, "V %d not in [1, 2^20]", V);
+    if (ld < V || ld > ((int64_t)1 << 31)) return fail(DS4MOE_E_SHAPE, "ld %lld for rows of %d", (long long)ld, V);
+    if (ld_out < V || ld_out > ((int64_t)1 << 31))
+        return fail(DS4MOE_E_SHAPE, "ld_out %lld for rows of %d", (long long)ld_out, V);
+    if (!rules) return fail(DS4MOE_E_ARG, "rules is NULL");
+    const ds4moe_logit_rules& r = *rules;
+    REQ_PTR(logits);
+    REQ_PTR(out);
+    if (out == logits && (dtype != out_dtype || (B > 1 && ld != ld_out)))
+        return fail(DS4MOE_E_ARG, "out is logits itself with another type or stride");
+    ds4::LogitArgs a{};
+    if (r.history) {
+        if (r.n_history < 0) return fail(DS4MOE_E_SHAPE, "n_history %d", r.n_history);
+        REQ_PTR(r.history);
+        REQ_PTR(r.history_offsets);
+        OPT_PTR(r.prompt_len);
+        OPT_PTR(r.repetition);
+        OPT_PTR(r.presence);
+        OPT_PTR(r.frequency);
+        if (r.n_history > 0 && (r.repetition || r.presence || r.frequency)) {
+            a.history = r.history;
+            a.history_offsets = r.history_offsets;
+            a.prompt_len = r.prompt_len;
+            a.n_history = r.n_history;
+            a.repetition = r.repetition;
+            a.presence = r.presence;
+            a.frequency = r.frequency;
+        }
+    }
+    if (r.bias_token) {
+        if (r.n_bias < 0) return fail(DS4MOE_E_SHAPE, "n_bias %d", r.n_bias);
+        REQ_PTR(r.bias_token);
+        REQ_PTR(r.bias_value);
+        REQ_PTR(r.bias_offsets);
+        if (r.n_bias > 0) {
+            a.bias_token = r.bias_token;
+            a.bias_value = r.bias_value;
+            a.bias_offsets = r.bias_offsets;
+            a.n_bias = r.n_bias;
+        }
+    }
+    if (r.mask) {
+        const int64_t words = ((int64_t)V + 31) / 32;
+        REQ_PTR(r.mask);
+        OPT_PTR(r.mask_row);
+        a.mask_ld = r.mask_ld ? r.mask_ld : words;
+        if (a.mask_ld < words || a.mask_ld > ((int64_t)1 << 31))
+            return fail(DS4MOE_E_SHAPE, "mask_ld %lld for rows of %d tokens", (long long)a.mask_ld, V);
+        if (r.mask_rows < 0) return fail(DS4MOE_E_SHAPE, "mask_rows %d", r.mask_rows);
+        if (!r.mask_row && r.mask_rows < B)
+            return fail(DS4MOE_E_SHAPE, "%d mask rows for %d rows without mask_row", r.mask_rows, B);
+        a.mask = r.mask;
+        a.mask_row = r.mask_row;
+        a.mask_rows = r.mask_rows;
+    }
+    a.B = B;
+    a.V = V;
+    a.logits = logits;
+    a.out = out;
+    a.ld = ld;
+    a.ld_out = ld_out;
+    return hip_status(ds4::launch_adjust_logits(a, dtype == DS4MOE_DT_F32, out_dtype == DS4MOE_DT_F32,
+                                                static_cast<hipStream_t>(stream)),
+                      "adjust logits");
+}
+
 }  // extern "C"

@@ -206,4 +206,23 @@ hipError_t launch_rows_to_tokens(const TokenArgs& a, bool f32, hipStream_t s);
 hipError_t launch_route_backward(int T, int E, int k, const int32_t* idx, const float* w, const float* dw,
                                  float* dlogits, hipStream_t s);
 
+// Rules on rows of V logits before sampling (logits.hip).
+struct LogitArgs {
+    int B, V;
+    const void* logits;              // [B] rows ld elements apart
+    void* out;                       // [B] rows ld_out elements apart
+    int64_t ld, ld_out;
+    const int32_t *history, *history_offsets, *prompt_len;   // [n_history], [B+1], [B]
+    int n_history;
+    const float *repetition, *presence, *frequency;          // [B]
+    const int32_t *bias_token, *bias_offsets;                // [n_bias], [B+1]
+    const float* bias_value;
+    int n_bias;
+    const uint32_t* mask;            // [mask_rows] rows mask_ld words apart
+    const int32_t* mask_row;         // [B], null: row b
+    int64_t mask_ld;
+    int mask_rows;
+};
+hipError_t launch_adjust_logits(const LogitArgs& a, bool f32_in, bool f32_out, hipStream_t s);
+
 }  // namespace ds4

@@ -448,6 +448,52 @@ int ds4moe_grouped_matmul_backward(const ds4moe_matmul* m, int32_t rows, const v
  * or backward (1).  0 on invalid arguments, and where none is needed. */
 size_t ds4moe_matmul_workspace_bytes(const ds4moe_matmul* m, int32_t rows, int32_t backward);
 
+/* Rules on logits before sampling, row by row: for token v of row b, with c
+ * the number of its occurrences in the row's history and n that in the
+ * history's generated part,
+ *   1. c > 0:  l = l > 0 ? l / repetition[b] : l * repetition[b]
+ *   2. n > 0:  l = l - frequency[b] * n - presence[b]
+ *   3. l = l + v's bias, if the row's list names v (the last of several
+ *      entries for v stands; -infinity bans a token)
+ *   4. l = -infinity, unless v's bit is set in the row's mask
+ * in fp32, rounded once to the output.  Each rule is off where its pointer is
+ * NULL: history (1 and 2), repetition (1), presence and frequency (0),
+ * bias_token, mask.  A row whose mask leaves nothing is -infinity throughout
+ * (ds4moe_sample then gives token -1).  The pages' engine samples on the
+ * coordinator (see ds4moe_sample); these rules and their order are this
+ * library's reading.
+ * Lists are ragged: row b's history is history[history_offsets[b] ..
+ * history_offsets[b+1]-1] (oldest first), the first prompt_len[b] tokens of it
+ * the prompt (NULL or <= 0: all of it generated); its biases are bias_token and
+ * bias_value at bias_offsets[b] .. bias_offsets[b+1]-1.  Token ids outside
+ * [0, V) are skipped.  Offsets that are not ascending within the list's length
+ * leave their row an empty list.  Bit v % 32 of word v / 32 of mask row
+ * mask_row[b] (row b itself where mask_row is NULL) allows token v; mask rows
+ * are mask_ld words apart (0: none between them), and a mask_row outside
+ * [0, mask_rows) leaves row b without a mask. */
+typedef struct {
+    const int32_t* history;          /* [n_history] */
+    const int32_t* history_offsets;  /* [B+1]       */
+    const int32_t* prompt_len;       /* [B]         */
+    const float* repetition;         /* [B]         */
+    const float* presence;           /* [B]         */
+    const float* frequency;          /* [B]         */
+    const int32_t* bias_token;       /* [n_bias]    */
+    const float* bias_value;         /* [n_bias]    */
+    const int32_t* bias_offsets;     /* [B+1]       */
+    const uint32_t* mask;            /* [mask_rows] */
+    const int32_t* mask_row;         /* [B]         */
+    int64_t mask_ld;
+    int32_t n_history, n_bias, mask_rows;
+} ds4moe_logit_rules;
+
+/* out = the rules applied to logits: [B] rows of V, ld and ld_out elements
+ * apart (>= V; rows at any alignment), types dtype and out_dtype (F32 or BF16).
+ * out may be logits itself when type and stride agree; no other overlap.
+ * 1 <= B <= 32768, 1 <= V <= 2^20. */
+int ds4moe_adjust_logits(int32_t B, int32_t V, const void* logits, int64_t ld, int32_t dtype,
+                         const ds4moe_logit_rules* rules, void* out, int64_t ld_out, int32_t out_dtype, void* stream);
+
 /* Token sampling from logits, one given random number per row: for each row r
  * of B, over V tokens in (logit descending, index ascending) order with
  * weights w_i = exp((logit_i - max) / temperature[r]),
