@@ -21,6 +21,8 @@ __all__ = [
     "grouped_matmul_backward", "sample", "sample_workspace_bytes",
     "Rows", "make_rows", "dispatch", "dispatch_backward", "collect", "collect_backward", "route_backward",
     "LogitRules", "adjust_logits",
+    "MatmulInt8", "make_matmul_int8", "matmul_int8_workspace_bytes", "quantize_rows_int8", "linear_int8",
+    "grouped_matmul_int8",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libds4moe.so")
@@ -39,7 +41,8 @@ EXPORTS = (
     "ds4moe_linear", "ds4moe_linear_backward", "ds4moe_grouped_matmul", "ds4moe_grouped_matmul_backward",
     "ds4moe_matmul_workspace_bytes", "ds4moe_sample", "ds4moe_sample_workspace_bytes",
     "ds4moe_dispatch", "ds4moe_dispatch_backward", "ds4moe_collect", "ds4moe_collect_backward",
-    "ds4moe_route_backward", "ds4moe_adjust_logits",
+    "ds4moe_route_backward", "ds4moe_adjust_logits", "ds4moe_quantize_rows_int8", "ds4moe_linear_int8",
+    "ds4moe_grouped_matmul_int8", "ds4moe_matmul_int8_workspace_bytes",
 )
 
 WS_REGION = {"topk_idx": 0, "topk_w": 1, "offsets": 2, "sorted_pair": 3, "pair_pos": 4, "active": 5,
@@ -61,6 +64,11 @@ class Weights(ctypes.Structure):
 class Matmul(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("in_dim", "out_dim", "groups", "dtype", "act", "grad_dtype")] +
                 [(n, ctypes.c_int64) for n in ("ldx", "ldw", "ldy", "ldz")])
+
+
+class MatmulInt8(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("in_dim", "out_dim", "groups", "dtype", "act")] +
+                [(n, ctypes.c_int64) for n in ("ldx", "ldw", "ldy")])
 
 
 class Rows(ctypes.Structure):
@@ -92,7 +100,7 @@ def _load():
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     cfgp, wp = ctypes.POINTER(Config), ctypes.POINTER(Weights)
-    mmp, rwp = ctypes.POINTER(Matmul), ctypes.POINTER(Rows)
+    mmp, m8p, rwp = ctypes.POINTER(Matmul), ctypes.POINTER(MatmulInt8), ctypes.POINTER(Rows)
     sigs = {
         "ds4moe_router_logits": (i32, [cfgp, i32, vp, vp, vp, vp]),
         "ds4moe_route": (i32, [cfgp, i32, vp, vp, vp, vp]),
@@ -123,6 +131,10 @@ def _load():
         "ds4moe_dispatch_backward": (i32, [rwp, i32, i32, vp, vp, vp, vp, vp, vp, vp]),
         "ds4moe_collect_backward": (i32, [rwp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
         "ds4moe_adjust_logits": (i32, [i32, i32, vp, i64, i32, ctypes.POINTER(LogitRules), vp, i64, i32, vp]),
+        "ds4moe_quantize_rows_int8": (i32, [i32, i32, i32, vp, i64, vp, i64, vp, vp]),
+        "ds4moe_linear_int8": (i32, [m8p, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "ds4moe_grouped_matmul_int8": (i32, [m8p, i32, vp, vp, i32, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]),
+        "ds4moe_matmul_int8_workspace_bytes": (sz, [m8p, i32]),
         "ds4moe_route_backward": (i32, [cfgp, i32, vp, vp, vp, vp, vp]),
     }
     for name, (res, args) in sigs.items():
@@ -416,6 +428,77 @@ def grouped_matmul_backward(m, rows, x, w, expert_offsets, dy, z=None, sorted_pa
         _vector("expert_offsets", expert_offsets, i32, m.groups + 1, dev),
         _vector("sorted_pair", sorted_pair, i32, rows, dev), top_k, _matrix("dx", dx, dt, rows, k, ldx, dev),
         _matrix("dw", dw, gd, wrows, k, ldw, dev), _vector("dbias", dbias, gd, wrows, dev), ws, nws, _s(stream, dev)))
+
+
+# ---- products in 8-bit integers ------------------------------------------------
+
+def make_matmul_int8(in_dim, out_dim, groups=1, dtype="bf16", act="none", ldx=0, ldw=0, ldy=0) -> MatmulInt8:
+    """Descriptor of a dense or grouped product in 8-bit integers: codes of the
+    weights [groups][out_dim][in_dim], `dtype` the type of bias, residual and y,
+    row strides in elements (0: no gaps)."""
+    return MatmulInt8(in_dim, out_dim, groups, DTYPE[dtype], ACT[act], ldx, ldw, ldy)
+
+
+def matmul_int8_workspace_bytes(m: MatmulInt8, rows: int) -> int:
+    return int(lib.ds4moe_matmul_int8_workspace_bytes(ctypes.byref(m), rows))
+
+
+def _row_stride(t, cols):
+    """Elements between the rows of a matrix (`cols`, where there is one row)."""
+    return t.stride(-2) if t.dim() > 1 and t.shape[-2] > 1 else cols
+
+
+def quantize_rows_int8(rows, cols, x, codes, scale, stream=None):
+    """codes [rows][cols] (int8) and scale [rows] (fp32) of the rows of x (fp32 or
+    bf16); rows of x and codes may be any multiple of 16 bytes apart."""
+    import torch
+    f32, dev = torch.float32, _here()
+    if x.dtype not in (f32, torch.bfloat16):
+        raise Ds4MoeError(-1, f"x is {x.dtype}, not {f32} or {torch.bfloat16}")
+    ldx, ldq = _row_stride(x, cols), _row_stride(codes, cols)
+    if rows == 1:    # (a single row has no stride to be off)
+        ldx, ldq = -(-cols // 8) * 8, -(-cols // 16) * 16
+    _check(lib.ds4moe_quantize_rows_int8(
+        rows, cols, int(x.dtype != f32), _matrix("x", x, x.dtype, rows, cols, ldx, dev), ldx,
+        _matrix("codes", codes, torch.int8, rows, cols, ldq, dev), ldq, _vector("scale", scale, f32, rows, dev),
+        _s(stream, dev)))
+
+
+def _m8_plan(m):
+    """As _mm_plan, without the gradients' type."""
+    import torch
+    types = (torch.float32, torch.bfloat16)
+    return (types[m.dtype] if 0 <= m.dtype <= 1 else None, torch.int8, torch.float32, m.groups * m.out_dim,
+            m.out_dim // 2 if m.act == ACT["swiglu"] else m.out_dim, _here())
+
+
+def linear_int8(m, rows, x, x_scale, w, w_scale, y, bias=None, residual=None, workspace=None, stream=None):
+    """y = act((x W^T) x_scale w_scale + bias) + residual on int8 codes x and w
+    with an fp32 scale for each of their rows."""
+    dt, i8, f32, wrows, oc, dev = _m8_plan(m)
+    k, ldy = m.in_dim, m.ldy
+    ws, nws = _workspace(workspace, dev)
+    _check(lib.ds4moe_linear_int8(
+        ctypes.byref(m), rows, _matrix("x", x, i8, rows, k, m.ldx, dev), _vector("x_scale", x_scale, f32, rows, dev),
+        _matrix("w", w, i8, wrows, k, m.ldw, dev), _vector("w_scale", w_scale, f32, wrows, dev),
+        _vector("bias", bias, dt, wrows, dev), _matrix("residual", residual, dt, rows, oc, ldy, dev),
+        _matrix("y", y, dt, rows, oc, ldy, dev), ws, nws, _s(stream, dev)))
+
+
+def grouped_matmul_int8(m, rows, x, x_scale, w, w_scale, expert_offsets, y, sorted_pair=None, top_k=1, x_rows=None,
+                        bias=None, workspace=None, stream=None):
+    """linear_int8 by expert: rows, expert_offsets, sorted_pair, top_k and x_rows
+    as in grouped_matmul; x_scale has a scale for each row of x."""
+    import torch
+    dt, i8, f32, wrows, oc, dev = _m8_plan(m)
+    k, xr, i32 = m.in_dim, _x_rows(x, rows) if x_rows is None else x_rows, torch.int32
+    ws, nws = _workspace(workspace, dev)
+    _check(lib.ds4moe_grouped_matmul_int8(
+        ctypes.byref(m), rows, _matrix("x", x, i8, xr, k, m.ldx, dev), _vector("x_scale", x_scale, f32, xr, dev), xr,
+        _matrix("w", w, i8, wrows, k, m.ldw, dev), _vector("w_scale", w_scale, f32, wrows, dev),
+        _vector("bias", bias, dt, wrows, dev), _vector("expert_offsets", expert_offsets, i32, m.groups + 1, dev),
+        _vector("sorted_pair", sorted_pair, i32, rows, dev), top_k, _matrix("y", y, dt, rows, oc, m.ldy, dev), ws, nws,
+        _s(stream, dev)))
 
 
 # ---- rows by expert and back ---------------------------------------------------

@@ -10,6 +10,7 @@
 #include "ds4moe.h"
 #include "launch.hpp"
 #include "matmul.hpp"
+#include "matmul_int8.hpp"
 
 namespace ds4 {
 thread_local StageEvents g_stage_events[N_STAGES] = {};
@@ -526,6 +527,87 @@ int mm_backward(const ds4moe_matmul* m, ds4::MmArgs& a, void* ws, size_t bytes, 
     }
     if (a.dw) TRY(hip_status(ds4::launch_mm_wgrad(a, f32, s), "matmul backward: dw"));
     return ok();
+}
+
+// The descriptor of a product in 8-bit integers as one of the others, which
+// has the limits that both share.
+ds4moe_matmul m8_as_mm(const ds4moe_matmul_int8* m) {
+    ds4moe_matmul o{};
+    o.in_dim = m->in_dim;
+    o.out_dim = m->out_dim;
+    o.groups = m->groups;
+    o.dtype = m->dtype;
+    o.act = m->act;
+    o.grad_dtype = m->dtype;
+    return o;
+}
+
+int check_m8(const ds4moe_matmul_int8* m, int32_t rows) {
+    if (!m) return fail(DS4MOE_E_ARG, "m is NULL");
+    const ds4moe_matmul mm = m8_as_mm(m);
+    TRY(check_mm(&mm, rows));
+    if (m->in_dim > 131071) return fail(DS4MOE_E_SHAPE, "in_dim %d above 131071", m->in_dim);
+    return DS4MOE_OK;
+}
+
+struct M8Layout {
+    size_t plan, split, total;
+};
+
+M8Layout m8_layout(const ds4moe_matmul_int8* m, int32_t rows, bool call) {
+    M8Layout L{};
+    const ds4moe_matmul mm = m8_as_mm(m);
+    if (m->groups > 1)
+        L.split = align256(256 + sizeof(ds4::MmChunk) * (size_t)mm_max_chunks(&mm, rows, ds4::MM_MIN_CHUNK));
+    L.total = align256(L.split + ds4::m8_split_bytes(rows, m->in_dim, m->out_dim, m->groups, call));
+    return L;
+}
+
+// Checks and launches a product in 8-bit integers whose rows and groups are in `a`.
+int m8_call(const ds4moe_matmul_int8* m, int32_t rows, ds4::M8Args& a, const int8_t* xq, const float* x_scale,
+            const int8_t* wq, const float* w_scale, const void* bias, const void* residual, void* y, void* workspace,
+            size_t workspace_bytes, hipStream_t s) {
+    const int64_t oc = m->act == DS4MOE_ACT_SWIGLU ? m->out_dim / 2 : m->out_dim;
+    a.P = rows;
+    a.K = m->in_dim;
+    a.N = m->out_dim;
+    a.E = m->groups;
+    a.act = m->act;
+    a.ldx = m->ldx ? m->ldx : m->in_dim;
+    a.ldw = m->ldw ? m->ldw : m->in_dim;
+    a.ldy = m->ldy ? m->ldy : oc;
+    TRY(check_ld("ldx", a.ldx, m->in_dim, 16));
+    TRY(check_ld("ldw", a.ldw, m->in_dim, 16));
+    TRY(check_ld("ldy", a.ldy, oc, m->dtype == DS4MOE_DT_F32 ? 4 : 8));
+    REQ_PTR(xq);
+    REQ_PTR(x_scale);
+    REQ_PTR(wq);
+    REQ_PTR(w_scale);
+    OPT_PTR(bias);
+    OPT_PTR(residual);
+    REQ_PTR(y);
+    a.x = xq;
+    a.xs = x_scale;
+    a.w = wq;
+    a.ws = w_scale;
+    a.bias = bias;
+    a.residual = residual;
+    a.y = y;
+    const M8Layout L = m8_layout(m, rows, true);
+    TRY(check_workspace(workspace, workspace_bytes, L.total));
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.ipart = reinterpret_cast<int32_t*>(ws + L.split);
+    const int bm = m->groups > 1 ? ds4::m8_chunk_rows(a.P, a.K, a.N, a.E) : 0;
+    if (bm) {
+        const ds4moe_matmul mm = m8_as_mm(m);
+        int32_t* n = reinterpret_cast<int32_t*>(ws + L.plan);
+        ds4::MmChunk* c = reinterpret_cast<ds4::MmChunk*>(ws + L.plan + 256);
+        a.max_chunks = mm_max_chunks(&mm, rows, bm);
+        TRY(hip_status(ds4::launch_mm_plan(a, bm, c, n, s), "matmul int8: plan"));
+        a.chunks = c;
+        a.n_chunks = n;
+    }
+    return hip_status(ds4::launch_m8(a, m->dtype == DS4MOE_DT_F32, s), "matmul int8");
 }
 
 }  // namespace
@@ -1071,6 +1153,61 @@ int ds4moe_adjust_logits(int32_t B, int32_t V, const void* logits, int64_t ld, i
     return hip_status(ds4::launch_adjust_logits(a, dtype == DS4MOE_DT_F32, out_dtype == DS4MOE_DT_F32,
                                                 static_cast<hipStream_t>(stream)),
                       "adjust logits");
+}
+
+int ds4moe_quantize_rows_int8(int32_t rows, int32_t cols, int32_t dtype, const void* x, int64_t ldx, int8_t* codes,
+                              int64_t ldq, float* scale, void* stream) {
+    if (dtype != DS4MOE_DT_F32 && dtype != DS4MOE_DT_BF16) {
+        if (dtype == DS4MOE_DT_FP8_E4M3) return fail(DS4MOE_E_UNSUPPORTED, "fp8 rows");
+        return fail(DS4MOE_E_ARG, "dtype %d", dtype);
+    }
+    if (rows < 1 || rows > (1 << 24)) return fail(DS4MOE_E_SHAPE, "rows %d not in [1, 2^24]", rows);
+    if (cols < 1 || cols > (1 << 20)) return fail(DS4MOE_E_SHAPE, "cols %d not in [1, 2^20]", cols);
+    if (!ldx) ldx = cols;
+    if (!ldq) ldq = cols;
+    TRY(check_ld("ldx", ldx, cols, dtype == DS4MOE_DT_F32 ? 4 : 8));
+    TRY(check_ld("ldq", ldq, cols, 16));
+    REQ_PTR(x);
+    REQ_PTR(codes);
+    REQ_PTR(scale);
+    return hip_status(ds4::launch_quantize_rows(rows, cols, dtype == DS4MOE_DT_F32, x, ldx, codes, ldq, scale,
+                                                static_cast<hipStream_t>(stream)),
+                      "quantize rows");
+}
+
+size_t ds4moe_matmul_int8_workspace_bytes(const ds4moe_matmul_int8* m, int32_t rows) {
+    if (check_m8(m, rows) != DS4MOE_OK) return 0;
+    return m8_layout(m, rows, false).total;
+}
+
+int ds4moe_linear_int8(const ds4moe_matmul_int8* m, int32_t rows, const int8_t* xq, const float* x_scale,
+                       const int8_t* wq, const float* w_scale, const void* bias, const void* residual, void* y,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    TRY(check_m8(m, rows));
+    if (m->groups != 1) return fail(DS4MOE_E_SHAPE, "linear has one group, not %d", m->groups);
+    ds4::M8Args a{};
+    a.x_rows = rows;
+    a.top_k = 1;
+    return m8_call(m, rows, a, xq, x_scale, wq, w_scale, bias, residual, y, workspace, workspace_bytes,
+                   static_cast<hipStream_t>(stream));
+}
+
+int ds4moe_grouped_matmul_int8(const ds4moe_matmul_int8* m, int32_t rows, const int8_t* xq, const float* x_scale,
+                               int32_t x_rows, const int8_t* wq, const float* w_scale, const void* bias,
+                               const int32_t* expert_offsets, const int32_t* sorted_pair, int32_t top_k, void* y,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+    TRY(check_m8(m, rows));
+    const ds4moe_matmul mm = m8_as_mm(m);
+    TRY(check_groups(&mm, rows, x_rows, sorted_pair, top_k));
+    REQ_PTR(expert_offsets);
+    OPT_PTR(sorted_pair);
+    ds4::M8Args a{};
+    a.offsets = expert_offsets;
+    a.sorted_pair = sorted_pair;
+    a.x_rows = x_rows;
+    a.top_k = sorted_pair ? top_k : 1;
+    return m8_call(m, rows, a, xq, x_scale, wq, w_scale, bias, nullptr, y, workspace, workspace_bytes,
+                   static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

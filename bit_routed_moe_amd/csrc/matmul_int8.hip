@@ -1,0 +1,453 @@
+// Products in 8-bit integers on the matrix cores (v_mfma_i32_16x16x64_i8).
+//
+// A workgroup computes BR x BC outputs in stages of 128 contraction columns
+// (128 bytes of every tile row), which global_load_lds_dwordx4 brings into a
+// ring of LDS buffers.  Tile row r's 16-byte chunk c lies in slot
+// c ^ ((r >> 1) & 7), so a fragment read (16 rows at one chunk per lane
+// quarter) covers all 64 banks.  One barrier per stage; in the 256-wide tiles
+// fragments are read one step of 64 columns ahead of the matrix instructions
+// that take them.  The column operand goes first into the matrix instruction,
+// so a lane holds 4 consecutive columns of one row; results leave through LDS
+// in whole rows.
+#include "matmul_int8.hpp"
+#include "tile.hpp"
+
+namespace ds4 {
+
+namespace {
+
+constexpr int M8_K = 128;          // contraction columns per stage
+constexpr int M8_MAX_SPLITS = 16;  // of the contraction
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
+// One operand of BT tile rows staged by NW waves.
+template <int BT, int NW>
+struct M8Operand {
+    static constexpr int BYTES = BT * M8_K;
+    static constexpr int ND = BYTES / 1024 / NW;   // DMAs per wave and stage
+    static_assert(ND * NW * 1024 == BYTES, "whole DMAs per wave");
+    // tile row and chunk that DMA i of wave w brings for this lane
+    static __device__ __forceinline__ int row(int i, int w, int lane) { return (i * NW + w) * 8 + (lane >> 3); }
+    static __device__ __forceinline__ int chunk(int row, int lane) { return (lane & 7) ^ ((row >> 1) & 7); }
+    // Fragment t (16 tile rows from t0 + 16 * t on) of k-step ks.
+    static __device__ __forceinline__ i32x4 frag(const uint8_t* buf, int t0, int t, int ks, int lane) {
+        const int m = lane & 15, q = lane >> 4, r = t0 + 16 * t + m;
+        return *reinterpret_cast<const i32x4*>(buf + r * 128 + (((ks * 4 + q) ^ (m >> 1)) << 4));
+    }
+    // Zeros from contraction column krem of the stage on (of one operand: the
+    // other's bytes there are then multiplied by zero).
+    static __device__ __forceinline__ void clear_tail(uint8_t* buf, int krem, int tid) {
+        for (int i = tid; i < BT * 8; i += NW * 64) {
+            const int r = i >> 3, c = i & 7;
+            uint8_t* p = buf + r * 128 + ((c ^ ((r >> 1) & 7)) << 4);
+            if (16 * c >= krem)
+                *reinterpret_cast<u32x4*>(p) = u32x4{0, 0, 0, 0};
+            else
+                for (int j = krem - 16 * c; j < 16; ++j) p[j] = 0;
+        }
+    }
+};
+
+// 8 sums of a row from a wave's LDS region: rows of CW values, 16-byte chunk c
+// of row r at c ^ r (modulo the row's chunks).
+template <int CW>
+__device__ __forceinline__ void m8_get8(const uint8_t* reg, int r, int col, int32_t (&v)[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const i32x4 x = *reinterpret_cast<const i32x4*>(reg + r * (CW * 4) + ((((col >> 2) + h) ^ (r & (CW / 4 - 1))) << 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * h + i] = x[i];
+    }
+}
+
+__device__ __forceinline__ void m8_part8(int32_t* p, const int32_t (&v)[8], int n, bool vec) {
+    if (vec) {
+        reinterpret_cast<i32x4*>(p)[0] = i32x4{v[0], v[1], v[2], v[3]};
+        reinterpret_cast<i32x4*>(p)[1] = i32x4{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = v[i];
+    }
+}
+
+// WR x WC waves, each (BR / WR) x (BC / WC) outputs; ST stage buffers.
+template <int BR, int BC, int WR, int WC, int ST, typename T>
+__global__ __launch_bounds__(64 * WR * WC) void m8_kernel(M8Args a, int tr, int tc) {
+    constexpr int NW = WR * WC;
+    using RowOp = M8Operand<BR, NW>;
+    using ColOp = M8Operand<BC, NW>;
+    constexpr int STB = RowOp::BYTES + ColOp::BYTES;
+    constexpr int MI = BR / WR / 16, NI = BC / WC / 16;
+    constexpr int LPS = RowOp::ND + ColOp::ND;   // DMAs per wave and stage
+    constexpr bool PIPE = BC == 256;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[ST * STB];
+    const uint32_t lds32 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    // this workgroup's tile: each of the 8 XCDs (workgroup id modulo 8) takes
+    // a contiguous eighth of the tiles that exist
+    const int ntr = a.chunks ? a.n_chunks[0] : tr;
+    const int total = ntr * tc, per = (total + 7) >> 3, slot = (int)blockIdx.x >> 3;
+    const int t = ((int)blockIdx.x & 7) * per + slot;
+    if (slot >= per || t >= total) return;
+    int rt, ct;
+    mt_tile(t, ntr, tc, rt, ct);
+    const int c0 = ct * BC;
+    MmChunk ch;
+    if (!mm_chunk(a, rt, BR, ch)) return;
+    const bool glu = a.act == MM_SWIGLU;
+    const int8_t* const wg = static_cast<const int8_t*>(a.w) + (size_t)ch.group * a.N * a.ldw;
+
+    // the DMAs' source rows; a lane's chunk is the same in all of a wave's
+    // DMAs, whose rows differ by a multiple of 16
+    static_assert((NW * 8) % 16 == 0, "one chunk per lane");
+    const int rrow = RowOp::row(0, w, lane), crow = ColOp::row(0, w, lane);
+    const int chunk = RowOp::chunk(rrow, lane);   // (rrow == crow)
+    const int8_t* rsrc[RowOp::ND];
+    const int8_t* csrc[ColOp::ND];
+#pragma unroll
+    for (int i = 0; i < RowOp::ND; ++i)
+        rsrc[i] = static_cast<const int8_t*>(a.x) +
+                  (size_t)mm_src(a, ch.row0 + min(rrow + i * NW * 8, ch.n - 1)) * a.ldx;
+#pragma unroll
+    for (int i = 0; i < ColOp::ND; ++i) {
+        const int n = mm_col(a, glu, c0, crow + i * NW * 8);
+        csrc[i] = wg + (size_t)(n < 0 ? a.N - 1 : n) * a.ldw;
+    }
+    const int kchunk = (a.K - 1) / 16;
+    auto issue1 = [&](int st, int i) {   // DMA i (0 .. LPS-1) of stage st
+        const uint32_t buf = lds32 + (uint32_t)(st % ST) * STB;
+        const int off = 16 * min(st * (M8_K / 16) + chunk, kchunk);
+        if (i < RowOp::ND)
+            mt_dma16(rsrc[i] + off, buf + (uint32_t)(i * NW + w) * 1024u);
+        else
+            mt_dma16(csrc[i - RowOp::ND] + off, buf + RowOp::BYTES + (uint32_t)((i - RowOp::ND) * NW + w) * 1024u);
+    };
+    auto issue = [&](int st) {
+#pragma unroll
+        for (int i = 0; i < LPS; ++i) issue1(st, i);
+    };
+
+    i32x4 acc[NI][MI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < MI; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    const int wr0 = (w % WR) * (BR / WR), wc0 = (w / WR) * (BC / WC);
+    // stages [sb, ns) of the contraction: all, or this split's share
+    const int nall = (a.K + M8_K - 1) / M8_K;
+    const int each = (nall + a.ksplits - 1) / a.ksplits;
+    const int sb = min(nall, (int)blockIdx.z * each), ns = min(nall, sb + each);
+    auto clear_tail = [&](int st) {   // behind the contraction's end, in the last stage
+        if (st == nall - 1 && a.K % M8_K) {
+            RowOp::clear_tail(lds + (st % ST) * STB, a.K % M8_K, tid);
+            __syncthreads();
+        }
+    };
+    // Matrix instructions on fragments rf, cf while the next ones are read
+    // from step ks of stage st (and, with more, stage `more`'s DMAs issued),
+    // spread over the row tiles.
+    auto step = [&](const i32x4 (&rf)[MI], const i32x4 (&cf)[NI], i32x4 (&rn)[MI], i32x4 (&cn)[NI], int st, int ks,
+                    int more) {
+        const uint8_t* buf = lds + (st % ST) * STB;
+#pragma unroll
+        for (int j = 0; j < MI; ++j) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (i * MI / NI == j) cn[i] = ColOp::frag(buf + RowOp::BYTES, wc0, i, ks, lane);
+            rn[j] = RowOp::frag(buf, wr0, j, ks, lane);
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cf[i], rf[j], acc[i][j], 0, 0, 0);
+            if (more >= 0) {
+#pragma unroll
+                for (int i = 0; i < LPS; ++i)
+                    if (i * MI / LPS == j) issue1(more, i);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    if constexpr (PIPE) {
+        if (sb < ns) {
+#pragma unroll
+            for (int s = 0; s < ST; ++s)
+                if (sb + s < ns) issue(sb + s);
+            if (sb + ST <= ns)
+                mt_wait_vm<(ST - 1) * LPS>();
+            else
+                mt_wait_vm<0>();
+            mt_barrier();
+            clear_tail(sb);
+            i32x4 rf[2][MI], cf[2][NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) cf[0][i] = ColOp::frag(lds + (sb % ST) * STB + RowOp::BYTES, wc0, i, 0, lane);
+#pragma unroll
+            for (int j = 0; j < MI; ++j) rf[0][j] = RowOp::frag(lds + (sb % ST) * STB, wr0, j, 0, lane);
+            for (int st = sb; st < ns; ++st) {
+                step(rf[0], cf[0], rf[1], cf[1], st, 1, -1);
+                // stage st is read; stage st + 1 has to have landed
+                if (ST > 2 && st + ST - 1 < ns)
+                    mt_wait_vm<(ST - 2) * LPS>();
+                else
+                    mt_wait_vm<0>();
+                mt_barrier();
+                if (st + 1 < ns) clear_tail(st + 1);
+                // (past the last stage the fragments read are not used)
+                step(rf[1], cf[1], rf[0], cf[0], st + 1, 0, st + ST < ns ? st + ST : -1);
+            }
+        }
+    } else {
+        if (sb < ns) {
+#pragma unroll
+            for (int s = 0; s < ST - 1; ++s)
+                if (sb + s < ns) issue(sb + s);
+        }
+        for (int st = sb; st < ns; ++st) {
+            if (ST > 2 && st + ST - 2 < ns)
+                mt_wait_vm<(ST - 2) * LPS>();
+            else
+                mt_wait_vm<0>();
+            mt_barrier();
+            if (st + ST - 1 < ns) issue(st + ST - 1);
+            clear_tail(st);
+            const uint8_t* buf = lds + (st % ST) * STB;
+#pragma unroll
+            for (int ks = 0; ks < M8_K / 64; ++ks) {
+                i32x4 rf[MI], cf[NI];
+#pragma unroll
+                for (int i = 0; i < NI; ++i) cf[i] = ColOp::frag(buf + RowOp::BYTES, wc0, i, ks, lane);
+#pragma unroll
+                for (int j = 0; j < MI; ++j) rf[j] = RowOp::frag(buf, wr0, j, ks, lane);
+#pragma unroll
+                for (int j = 0; j < MI; ++j)
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cf[i], rf[j], acc[i][j], 0, 0, 0);
+            }
+        }
+    }
+
+    // Out through LDS, RP rows of the wave's tile at a time.  In the
+    // accumulators a lane holds columns 4q .. 4q+3 of row m of each 16 x 16
+    // block.
+    constexpr int CW = BC / WC, WROWS = BR / WR;
+    constexpr int FIT = ST * STB / NW / (CW * 4);   // rows of the wave's region
+    constexpr int RP = FIT >= WROWS ? WROWS : (FIT >= WROWS / 2 ? WROWS / 2 : WROWS / 4);
+    static_assert(RP >= 16 && RP % 16 == 0 && RP <= FIT && (CW & (CW - 1)) == 0 && CW >= 32, "passes of whole row tiles");
+    int32_t* const part = a.ksplits > 1 ? a.ipart + (size_t)blockIdx.z * a.kpart_stride : nullptr;
+    uint8_t* reg = lds + w * (RP * CW * 4);
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < WROWS / RP; ++p) {
+        const int m = lane & 15, q = lane >> 4;
+#pragma unroll
+        for (int j = 0; j < RP / 16; ++j)
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                *reinterpret_cast<i32x4*>(reg + (16 * j + m) * (CW * 4) + (((4 * i + q) ^ (m & (CW / 4 - 1))) << 4)) =
+                    acc[i][p * (RP / 16) + j];
+        const int rbase = wr0 + p * RP;
+        if (glu) {
+            // 16 gate columns, then the 16 up columns they pair with
+            constexpr int LR = CW / 16;   // lanes per row
+            const int half = a.N >> 1;
+            const int c8 = lane & (LR - 1), col = 32 * (c8 >> 1) + 8 * (c8 & 1);
+            const int f = ((c0 + wc0) >> 1) + 8 * c8, cnt = half - f;
+#pragma unroll 1
+            for (int rr = lane / LR; rr < RP; rr += 64 / LR) {
+                int32_t g[8], u[8];
+                m8_get8<CW>(reg, rr, col, g);
+                m8_get8<CW>(reg, rr, col + 16, u);
+                if (rbase + rr >= ch.n || cnt <= 0) continue;
+                const int r = ch.row0 + rbase + rr;
+                if (part) {
+                    int32_t* o = part + (size_t)r * a.ldp + f;
+                    m8_part8(o, g, cnt, cnt >= 8);
+                    m8_part8(o + half, u, cnt, cnt >= 8 && (half & 3) == 0);
+                } else {
+                    const float xs = a.xs[mm_src(a, r)];
+                    float zg[8], zu[8];
+                    m8_z8<T>(a, ch.group, xs, f, cnt, g, zg);
+                    m8_z8<T>(a, ch.group, xs, half + f, cnt, u, zu);
+                    m8_out8<T, true>(a, r, f, cnt, zg, zu);
+                }
+            }
+        } else {
+            constexpr int LR = CW / 8;
+            const int col = 8 * (lane & (LR - 1)), n = c0 + wc0 + col, cnt = a.N - n;
+#pragma unroll 1
+            for (int rr = lane / LR; rr < RP; rr += 64 / LR) {
+                int32_t v[8];
+                m8_get8<CW>(reg, rr, col, v);
+                if (rbase + rr >= ch.n || cnt <= 0) continue;
+                const int r = ch.row0 + rbase + rr;
+                if (part) {
+                    m8_part8(part + (size_t)r * a.ldp + n, v, cnt, cnt >= 8);
+                } else {
+                    float z[8];
+                    m8_z8<T>(a, ch.group, a.xs[mm_src(a, r)], n, cnt, v, z);
+                    m8_out8<T, false>(a, r, n, cnt, z, nullptr);
+                }
+            }
+        }
+    }
+}
+
+// Joins the splits of a product and finishes the rows as the tile kernel
+// would: 8 rows of 256 columns per workgroup, rows 8 * blockIdx.z on of one
+// chunk.
+template <typename T>
+__global__ __launch_bounds__(256) void m8_join_kernel(M8Args a, int bm) {
+    MmChunk ch;
+    if (!mm_chunk(a, blockIdx.y, bm, ch)) return;
+    const int rr = blockIdx.z * 8 + (threadIdx.x >> 5);
+    if (rr >= ch.n) return;
+    const int r = ch.row0 + rr, half = a.N >> 1;
+    const bool glu = a.act == MM_SWIGLU;
+    const int n = blockIdx.x * 256 + 8 * (threadIdx.x & 31), cnt = (glu ? half : a.N) - n;
+    if (cnt <= 0) return;
+    auto sum8 = [&](int c, bool vec, int32_t (&v)[8]) {
+        const int32_t* p = a.ipart + (size_t)r * a.ldp + c;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0;
+        if (vec) {
+#pragma unroll 4
+            for (int s = 0; s < a.ksplits; ++s) {
+                const i32x4* x = reinterpret_cast<const i32x4*>(p + s * a.kpart_stride);
+                const i32x4 lo = x[0], hi = x[1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] += lo[i];
+                    v[4 + i] += hi[i];
+                }
+            }
+        } else {
+            for (int s = 0; s < a.ksplits; ++s)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < cnt) v[i] += p[s * a.kpart_stride + i];
+        }
+    };
+    const float xs = a.xs[mm_src(a, r)];
+    int32_t v[8];
+    float z[8];
+    sum8(n, cnt >= 8, v);
+    m8_z8<T>(a, ch.group, xs, n, cnt, v, z);
+    if (glu) {
+        float u[8];
+        sum8(half + n, cnt >= 8 && (half & 3) == 0, v);
+        m8_z8<T>(a, ch.group, xs, half + n, cnt, v, u);
+        m8_out8<T, true>(a, r, n, cnt, z, u);
+    } else {
+        m8_out8<T, false>(a, r, n, cnt, z, nullptr);
+    }
+}
+
+int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// Tile shapes, with the times that the estimate takes (us per stage of 128
+// contraction columns): lat of a workgroup by itself on its CU, thr per
+// workgroup and CU when the chip is full; wgs that share a CU.
+struct M8Shape {
+    int br, bc;
+    double lat, thr;
+    int wgs;
+};
+constexpr M8Shape M8_SHAPES[] = {
+    {256, 256, 1.1, 1.6, 1}, {128, 256, 0.68, 0.95, 1}, {128, 128, 0.55, 0.55, 2}, {64, 64, 0.25, 0.18, 3}};
+constexpr int M8_NSHAPES = 4;
+constexpr double M8_ENDS = 3.0;    // us to fill a workgroup's first stages and to write its tile
+constexpr double M8_JOIN = 4.0;    // us of a join launch
+constexpr double M8_MEM = 4.5e6;   // bytes per us, of outputs and partial sums
+constexpr double M8_RAGGED = 1.25; // small tiles of groups read their weights more often
+
+struct M8Pick {
+    int shape, splits;
+};
+
+// Tile shape and contraction splits of the least estimated time: a CU's
+// workgroups times their stages, plus what does not overlap.
+M8Pick m8_pick(int P, int K, int N, int E) {
+    const int live = E < P ? E : P;
+    const int ns = cdiv(K, M8_K);
+    M8Pick best{0, 1};
+    double least = 1e300;
+    for (int i = 0; i < M8_NSHAPES; ++i) {
+        const M8Shape& t = M8_SHAPES[i];
+        double tr = cdiv(P, t.br);   // row tiles; of ragged groups about half a tile each is not filled
+        if (E > 1) tr = (double)P / t.br + 0.5 * live > live ? (double)P / t.br + 0.5 * live : live;
+        const double tiles = tr * cdiv(N, t.bc);
+        const double out = tiles * t.br * t.bc * 2.0 / M8_MEM;
+        for (int s = 1; s <= M8_MAX_SPLITS && (s == 1 || (i >= 2 && ns / s >= 4 && tiles * s <= 512.0)); s *= 2) {
+            const double wgs = tiles * s, per_cu = wgs <= 256.0 ? wgs / 256.0 : (double)(int64_t)(wgs / 256.0 + 0.999);
+            const double thr = t.thr * (t.wgs > 1 && E > 1 ? M8_RAGGED : 1.0);
+            const double stage = thr * per_cu > t.lat ? thr * per_cu : t.lat;
+            double us = stage * cdiv(ns, s);
+            if (t.wgs == 1)
+                us += M8_ENDS * (per_cu < 1.0 ? 1.0 : per_cu) + out;
+            else
+                us = (us > out ? us : out) + M8_ENDS;
+            if (s > 1) us += M8_JOIN + (double)wgs * t.br * t.bc * 8.0 / M8_MEM;
+            if (us < least) {
+                least = us;
+                best = M8Pick{i, s};
+            }
+        }
+    }
+    return best;
+}
+
+template <int BR, int BC, int WR, int WC, int ST, typename T>
+hipError_t m8_launch(const M8Args& a, hipStream_t s) {
+    const int tr = a.chunks ? a.max_chunks : cdiv(a.P, BR), tc = cdiv(a.N, BC);
+    const int64_t total = (int64_t)tr * tc;
+    const dim3 g((uint32_t)((total + 7) / 8 * 8), 1, (uint32_t)a.ksplits);
+    m8_kernel<BR, BC, WR, WC, ST, T><<<g, 64 * WR * WC, 0, s>>>(a, tr, tc);
+    if (a.ksplits > 1) {
+        const dim3 j((uint32_t)cdiv(a.act == MM_SWIGLU ? a.N / 2 : a.N, 256), (uint32_t)tr, BR / 8u);
+        m8_join_kernel<T><<<j, 256, 0, s>>>(a, BR);
+    }
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t m8_run(const M8Args& a, int shape, hipStream_t s) {
+    switch (shape) {
+        case 0: return m8_launch<256, 256, 2, 4, 2, T>(a, s);
+        case 1: return m8_launch<128, 256, 2, 4, 3, T>(a, s);
+        case 2: return m8_launch<128, 128, 2, 2, 2, T>(a, s);
+        default: return m8_launch<64, 64, 2, 2, 3, T>(a, s);
+    }
+}
+
+}  // namespace
+
+int m8_chunk_rows(int P, int K, int N, int E) {
+    return m8_rows_takes(P, N, E) ? 0 : M8_SHAPES[m8_pick(P, K, N, E).shape].br;
+}
+
+size_t m8_split_bytes(int P, int K, int N, int E, bool exact) {
+    // the bound: at most 512 tiles of up to 128 x 128 in all splits together,
+    // and at most M8_MAX_SPLITS splits
+    if (cdiv(K, M8_K) < 8) return 0;
+    const int64_t one = (int64_t)P * ((N + 7) / 8 * 8);
+    if (exact) {
+        const int splits = m8_rows_takes(P, N, E) ? 1 : m8_pick(P, K, N, E).splits;
+        return splits > 1 ? (size_t)splits * one * 4 : 0;
+    }
+    const int64_t all = M8_MAX_SPLITS * one, cap = (int64_t)512 * 128 * 128;
+    return (size_t)(all < cap ? all : cap) * 4;
+}
+
+hipError_t launch_m8(const M8Args& a0, bool f32, hipStream_t s) {
+    if (m8_rows_takes(a0.P, a0.N, a0.E)) return launch_m8_rows(a0, f32, s);
+    M8Args a = a0;
+    const M8Pick pick = m8_pick(a.P, a.K, a.N, a.E);
+    a.ksplits = pick.splits;
+    a.ldp = (a.N + 7) / 8 * 8;
+    a.kpart_stride = (size_t)a.P * a.ldp;
+    return f32 ? m8_run<float>(a, pick.shape, s) : m8_run<uint16_t>(a, pick.shape, s);
+}
+
+}  // namespace ds4

@@ -1,0 +1,205 @@
+// 8-bit products of few rows (decoding): every weight is read once, straight
+// into registers, and the time is that of reading them.
+//
+// A workgroup takes one chunk of at most 16 rows of a group and 16 * RT weight
+// rows (SwiGLU: 16 gate rows and the 16 up rows they pair with); its 8 waves
+// share the contraction KW ways (and weight rows 8 / KW ways where the
+// contraction is short).  A step is 256 contraction columns, 4 loads of 64
+// contiguous bytes of each of 16 weight rows, two steps in flight per wave.
+// Weights go first into the matrix instruction (v_mfma_i32_16x16x64_i8), so a
+// lane's results belong to one row.  The waves' sums are joined in LDS.
+//
+// The rows' group is found from the offsets in the kernel (a plan launch would
+// cost more than the product): workgroup row p of the grid is sorted row p,
+// and only the first row of each 16-row chunk of a group goes on.
+#include "matmul_int8.hpp"
+
+namespace ds4 {
+
+namespace {
+
+constexpr int W8_WAVES = 8;
+constexpr int W8_STEP = 256;   // contraction columns per step
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
+// 16 bytes of a row from chunk c on; bytes from column K on are zero.
+__device__ __forceinline__ i32x4 w8_masked(const int8_t* row, int c, int K) {
+    i32x4 v = {0, 0, 0, 0};
+    const int n = K - 16 * c;
+    if (n > 0) {
+        v = *reinterpret_cast<const i32x4*>(row + 16 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int b = n - 4 * i;   // bytes of word i that exist
+            v[i] = b >= 4 ? v[i] : (b > 0 ? (int32_t)((uint32_t)v[i] & (0xFFFFFFFFu >> (32 - 8 * b))) : 0);
+        }
+    }
+    return v;
+}
+
+template <typename T, int RT, bool GLU>
+__global__ __launch_bounds__(64 * W8_WAVES) void w8_kernel(M8Args a, int kw) {
+    __shared__ i32x4 red[W8_WAVES][RT][64];
+    __shared__ int found[3];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int m = lane & 15, q = lane >> 4;
+
+    // the chunk: group, first row, rows
+    int group = 0, row0 = blockIdx.y, n = 0;
+    if (a.offsets) {
+        if (tid == 0) found[2] = 0;
+        __syncthreads();
+        for (int e = tid; e < a.E; e += 64 * W8_WAVES) {
+            int r0, cnt;
+            mm_group_rows(a.offsets, e, a.P, r0, cnt);
+            if (row0 >= r0 && row0 < r0 + cnt && (row0 - r0) % 16 == 0) {
+                // (overlapping ranges of corrupt offsets: the last one written)
+                found[0] = e;
+                found[1] = min(16, r0 + cnt - row0);
+                found[2] = 1;
+            }
+        }
+        __syncthreads();
+        if (!found[2]) return;
+        group = __builtin_amdgcn_readfirstlane(found[0]);
+        n = __builtin_amdgcn_readfirstlane(found[1]);
+    } else {
+        row0 = 16 * blockIdx.y;
+        n = min(16, a.P - row0);
+    }
+    n = min(n, a.P - row0);
+
+    // this wave's weight rows and share of the contraction
+    const int ng = W8_WAVES / kw, kpart = w % kw;
+    const int rb = blockIdx.x * ng + w / kw;               // block of 16 * RT rows (GLU: 16 pairs)
+    const int cols = GLU ? a.N >> 1 : a.N;
+    const int8_t* const wg = static_cast<const int8_t*>(a.w) + (size_t)group * a.N * a.ldw;
+    const int8_t* wr[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int c = GLU ? rb * 16 + m : rb * 16 * RT + 16 * t + m;
+        wr[t] = wg + (size_t)(min(c, cols - 1) + (GLU && t ? cols : 0)) * a.ldw;
+    }
+    const bool has = m < n;
+    const int8_t* const xr = static_cast<const int8_t*>(a.x) + (size_t)mm_src(a, row0 + (has ? m : 0)) * a.ldx;
+
+    const int full = a.K / W8_STEP;
+    const int each = (full + kw - 1) / kw;
+    const int s0 = min(full, kpart * each), s1 = min(full, s0 + each);
+    i32x4 acc[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t] = i32x4{0, 0, 0, 0};
+    i32x4 wv[2][RT][4], xv[2][4];
+    auto load = [&](int b, int s) {
+        const int c = s * W8_STEP + 16 * q;
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) wv[b][t][j] = reinterpret_cast<const i32x4*>(wr[t] + c)[4 * j];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            xv[b][j] = i32x4{0, 0, 0, 0};
+            if (has) xv[b][j] = reinterpret_cast<const i32x4*>(xr + c)[4 * j];
+        }
+    };
+    auto mma = [&](int b) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[b][t][j], xv[b][j], acc[t], 0, 0, 0);
+    };
+    if (rb * 16 * (GLU ? 1 : RT) < cols) {
+        if (s0 < s1) load(0, s0);
+        if (s0 + 1 < s1) load(1, s0 + 1);
+        for (int s = s0; s < s1; s += 2) {
+            mma(0);
+            if (s + 2 < s1) load(0, s + 2);
+            if (s + 1 < s1) {
+                mma(1);
+                if (s + 3 < s1) load(1, s + 3);
+            }
+        }
+        if (kpart == kw - 1 && a.K % W8_STEP) {   // the last columns, masked
+            const int c = full * (W8_STEP / 16) + q;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const i32x4 xt = has ? w8_masked(xr, c + 4 * j, a.K) : i32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                    acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w8_masked(wr[t], c + 4 * j, a.K), xt, acc[t], 0, 0, 0);
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) red[w][t][lane] = acc[t];
+    __syncthreads();
+
+    // one output per thread and turn: weight row rr (fastest) of row group g, row tok
+    const int per = GLU ? 16 : 16 * RT;                    // outputs per row group and row
+    for (int i = tid; i < ng * per * n; i += 64 * W8_WAVES) {
+        const int rr = i % per, g = (i / per) % ng, tok = i / (per * ng);
+        const int c = (blockIdx.x * ng + g) * per + rr;
+        if (c >= cols) continue;
+        const int r = row0 + tok;
+        const float xs = a.xs[mm_src(a, r)];
+        float z[GLU ? 2 : 1];
+#pragma unroll
+        for (int t = 0; t < (GLU ? 2 : 1); ++t) {
+            const int rt = GLU ? t : rr >> 4;
+            const int32_t* p = reinterpret_cast<const int32_t*>(&red[g * kw][rt][((rr & 15) >> 2) * 16 + tok]) + (rr & 3);
+            int32_t sum = 0;
+            for (int k = 0; k < kw; ++k) sum += p[(size_t)k * RT * 64 * 4];
+            const size_t o = (size_t)group * a.N + c + (t ? cols : 0);
+            z[t] = (float)sum * xs * a.ws[o];
+            if (a.bias) z[t] += mm_ld(static_cast<const T*>(a.bias) + o);
+        }
+        float v;
+        if constexpr (GLU)
+            v = z[0] / (1.0f + expf(-z[0])) * z[1];
+        else
+            v = mm_act(z[0], a.act);
+        const size_t o = (size_t)r * a.ldy + c;
+        if (a.residual) v += mm_ld(static_cast<const T*>(a.residual) + o);
+        mm_st(static_cast<T*>(a.y) + o, v);
+    }
+}
+
+// Waves of a workgroup along the contraction: all 8 from 8 steps on, fewer
+// while a share would be empty.
+int w8_kw(int K) {
+    int kw = W8_WAVES;
+    while (kw > 1 && kw > K / W8_STEP) kw >>= 1;
+    return kw;
+}
+
+template <typename T>
+hipError_t w8_run(const M8Args& a, hipStream_t s) {
+    const int kw = w8_kw(a.K), ng = W8_WAVES / kw;
+    const uint32_t gy = a.offsets ? (uint32_t)a.P : (uint32_t)((a.P + 15) / 16);
+    const bool glu = a.act == MM_SWIGLU;
+    // two row tiles per wave once there are 4 workgroups per CU with them
+    const bool two = glu || (int64_t)((a.N + 31) / 32) * (a.offsets ? a.P : 1) >= 1024 * ng;
+    const int per = glu ? 16 : (two ? 32 : 16), cols = glu ? a.N / 2 : a.N;
+    const dim3 g((uint32_t)((cols + per * ng - 1) / (per * ng)), gy);
+    if (glu)
+        w8_kernel<T, 2, true><<<g, 64 * W8_WAVES, 0, s>>>(a, kw);
+    else if (two)
+        w8_kernel<T, 2, false><<<g, 64 * W8_WAVES, 0, s>>>(a, kw);
+    else
+        w8_kernel<T, 1, false><<<g, 64 * W8_WAVES, 0, s>>>(a, kw);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+bool m8_rows_takes(int P, int N, int E) {
+    if (E > 1) return P <= 16 || (P <= 256 && P <= 2 * E);
+    return P <= 8 || (P <= 16 && N < 32768);
+}
+
+hipError_t launch_m8_rows(const M8Args& a, bool f32, hipStream_t s) {
+    return f32 ? w8_run<float>(a, s) : w8_run<uint16_t>(a, s);
+}
+
+}  // namespace ds4

@@ -448,6 +448,61 @@ int ds4moe_grouped_matmul_backward(const ds4moe_matmul* m, int32_t rows, const v
  * or backward (1).  0 on invalid arguments, and where none is needed. */
 size_t ds4moe_matmul_workspace_bytes(const ds4moe_matmul* m, int32_t rows, int32_t backward);
 
+/* ---- products in 8-bit integers --------------------------------------------
+ * Products of rows with weights, both held in signed bytes with one fp32 scale
+ * for each row of x (token) and of w (output channel), dense or grouped by
+ * expert, with the epilogue of the products above:
+ *     z[r][n] = (sum_k xq[src(r)][k] * wq_e[n][k]) * x_scale[src(r)] * w_scale_e[n] + bias_e[n]
+ *     y[r]    = act(z[r]) + residual[r]
+ * Sums are exact, scales, bias and activation fp32, y is rounded once.  Every
+ * byte from -128 to 127 is a code.  The pages quantize only the routed experts
+ * (hysenlabs page, section above); these calls are for projections, heads and
+ * experts that a user keeps at 8 bits.
+ *
+ * ds4moe_quantize_rows_int8 makes codes and scales of `rows` rows of `cols`
+ * values (activations, or weights once): with top = max_k |x[r][k]|,
+ *     scale[r] = top / 127,  code = the whole number nearest to
+ *     x[r][k] * 127 / top (ties to even), decided without rounding;
+ * a row of zeros has scale 0 and codes 0, a row with a NaN or an infinity
+ * scale NaN (and codes 0), so that its products are NaN.
+ * x: [rows][ldx], dtype F32 or BF16; codes: [rows][ldq] bytes; scale fp32
+ * [rows].  ldx and ldq as the products' strides: 0 = no gaps, whole multiples
+ * of 16 bytes.  1 <= rows <= 2^24, 1 <= cols <= 2^20. */
+int ds4moe_quantize_rows_int8(int32_t rows, int32_t cols, int32_t dtype, const void* x, int64_t ldx, int8_t* codes,
+                              int64_t ldq, float* scale, void* stream);
+
+/* Strides: ldx and ldw in bytes, ldy (y, residual) in elements of dtype; the
+ * products' rules.  Limits: those of ds4moe_matmul, and in_dim <= 131071 (a
+ * sum of products of bytes then fits 32 bits). */
+typedef struct {
+    int32_t in_dim;      /* K: columns of xq                                  */
+    int32_t out_dim;     /* N: rows of a weight matrix                        */
+    int32_t groups;      /* experts (1 for ds4moe_linear_int8)                */
+    int32_t dtype;       /* of bias, residual and y: F32 or BF16              */
+    int32_t act;         /* ds4moe_act                                        */
+    int64_t ldx, ldw, ldy;
+} ds4moe_matmul_int8;
+
+/* xq [rows][ldx], x_scale [rows], wq [out_dim][ldw], w_scale [out_dim]; bias
+ * and residual may be NULL; y may be residual itself.  workspace: device
+ * scratch of ds4moe_matmul_int8_workspace_bytes(m, rows) bytes (NULL if 0). */
+int ds4moe_linear_int8(const ds4moe_matmul_int8* m, int32_t rows, const int8_t* xq, const float* x_scale,
+                       const int8_t* wq, const float* w_scale, const void* bias, const void* residual, void* y,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Rows by expert as in ds4moe_grouped_matmul: xq [x_rows][ldx] and x_scale
+ * [x_rows] are read through sorted_pair (or in order where it is NULL), wq
+ * [groups][out_dim][ldw], w_scale and bias [groups][out_dim]; rows outside
+ * every expert's range are left as they were. */
+int ds4moe_grouped_matmul_int8(const ds4moe_matmul_int8* m, int32_t rows, const int8_t* xq, const float* x_scale,
+                               int32_t x_rows, const int8_t* wq, const float* w_scale, const void* bias,
+                               const int32_t* expert_offsets, const int32_t* sorted_pair, int32_t top_k, void* y,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of both for up to `rows` rows (0 on invalid arguments, and
+ * where none is needed). */
+size_t ds4moe_matmul_int8_workspace_bytes(const ds4moe_matmul_int8* m, int32_t rows);
+
 /* Rules on logits before sampling, row by row: for token v of row b, with c
  * the number of its occurrences in the row's history and n that in the
  * history's generated part,
