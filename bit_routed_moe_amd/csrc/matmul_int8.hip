@@ -424,7 +424,7 @@ hipError_t m8_run(const M8Args& a, int shape, hipStream_t s) {
 }  // namespace
 
 int m8_chunk_rows(int P, int K, int N, int E) {
-    return m8_rows_takes(P, N, E) ? 0 : M8_SHAPES[m8_pick(P, K, N, E).shape].br;
+    return m8_rows_takes(P, K, N, E) ? 0 : M8_SHAPES[m8_pick(P, K, N, E).shape].br;
 }
 
 size_t m8_split_bytes(int P, int K, int N, int E, bool exact) {
@@ -433,7 +433,7 @@ size_t m8_split_bytes(int P, int K, int N, int E, bool exact) {
     if (cdiv(K, M8_K) < 8) return 0;
     const int64_t one = (int64_t)P * ((N + 7) / 8 * 8);
     if (exact) {
-        const int splits = m8_rows_takes(P, N, E) ? 1 : m8_pick(P, K, N, E).splits;
+        const int splits = m8_rows_takes(P, K, N, E) ? 1 : m8_pick(P, K, N, E).splits;
         return splits > 1 ? (size_t)splits * one * 4 : 0;
     }
     const int64_t all = M8_MAX_SPLITS * one, cap = (int64_t)512 * 128 * 128;
@@ -441,7 +441,7 @@ size_t m8_split_bytes(int P, int K, int N, int E, bool exact) {
 }
 
 hipError_t launch_m8(const M8Args& a0, bool f32, hipStream_t s) {
-    if (m8_rows_takes(a0.P, a0.N, a0.E)) return launch_m8_rows(a0, f32, s);
+    if (m8_rows_takes(a0.P, a0.K, a0.N, a0.E)) return launch_m8_rows(a0, f32, s);
     M8Args a = a0;
     const M8Pick pick = m8_pick(a.P, a.K, a.N, a.E);
     a.ksplits = pick.splits;

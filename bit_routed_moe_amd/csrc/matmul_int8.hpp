@@ -102,7 +102,7 @@ size_t m8_split_bytes(int P, int K, int N, int E, bool exact);
 hipError_t launch_m8(const M8Args& a, bool f32, hipStream_t s);
 
 // Products of few rows (matmul_int8_rows.hip).
-bool m8_rows_takes(int P, int N, int E);
+bool m8_rows_takes(int P, int K, int N, int E);
 hipError_t launch_m8_rows(const M8Args& a, bool f32, hipStream_t s);
 
 }  // namespace ds4

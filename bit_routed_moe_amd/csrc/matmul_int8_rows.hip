@@ -10,8 +10,9 @@
 // lane's results belong to one row.  The waves' sums are joined in LDS.
 //
 // The rows' group is found from the offsets in the kernel (a plan launch would
-// cost more than the product): workgroup row p of the grid is sorted row p,
-// and only the first row of each 16-row chunk of a group goes on.
+// cost more than the product), by a scan over the groups' numbers of chunks, or
+// where there are fewer rows than chunks could be, by row: workgroup row p of
+// the grid is sorted row p, and only the first row of each chunk goes on.
 #include "matmul_int8.hpp"
 
 namespace ds4 {
@@ -20,6 +21,7 @@ namespace {
 
 constexpr int W8_WAVES = 8;
 constexpr int W8_STEP = 256;   // contraction columns per step
+constexpr int W8_REREAD = 1 << 24;   // bytes of weights that all chunks together may read (m8_rows_takes)
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 // 16 bytes of a row from chunk c on; bytes from column K on are zero.
@@ -38,36 +40,57 @@ __device__ __forceinline__ i32x4 w8_masked(const int8_t* row, int c, int K) {
 }
 
 template <typename T, int RT, bool GLU>
-__global__ __launch_bounds__(64 * W8_WAVES) void w8_kernel(M8Args a, int kw) {
+__global__ __launch_bounds__(64 * W8_WAVES) void w8_kernel(M8Args a, int kw, int scan) {
     __shared__ i32x4 red[W8_WAVES][RT][64];
-    __shared__ int found[3];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = lane & 15, q = lane >> 4;
 
     // the chunk: group, first row, rows
-    int group = 0, row0 = blockIdx.y, n = 0;
+    int group = 0, row0, n;
     if (a.offsets) {
-        if (tid == 0) found[2] = 0;
-        __syncthreads();
-        for (int e = tid; e < a.E; e += 64 * W8_WAVES) {
-            int r0, cnt;
-            mm_group_rows(a.offsets, e, a.P, r0, cnt);
-            if (row0 >= r0 && row0 < r0 + cnt && (row0 - r0) % 16 == 0) {
-                // (overlapping ranges of corrupt offsets: the last one written)
-                found[0] = e;
-                found[1] = min(16, r0 + cnt - row0);
-                found[2] = 1;
+        __shared__ int found[4], tmp[32];
+        if (tid == 0) found[0] = 0;
+        if (scan) {   // chunk blockIdx.y of the groups' chunks
+            int r0[2], cnt[2], total;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                r0[i] = cnt[i] = 0;
+                if (2 * tid + i < a.E) mm_group_rows(a.offsets, 2 * tid + i, a.P, r0[i], cnt[i]);
+            }
+            const int n0 = (cnt[0] + 15) >> 4, n1 = (cnt[1] + 15) >> 4;
+            int at = (int)blockIdx.y - block_exclusive_scan(n0 + n1, tmp, &total);   // (barriers inside)
+            if (at >= 0 && at < n0 + n1) {
+                const int i = at >= n0;
+                at -= i ? n0 : 0;
+                found[0] = 1;
+                found[1] = 2 * tid + i;
+                found[2] = r0[i] + 16 * at;
+                found[3] = min(16, cnt[i] - 16 * at);
+            }
+        } else {      // the chunk that starts at row blockIdx.y, if one does
+            __syncthreads();
+            for (int e = tid; e < a.E; e += 64 * W8_WAVES) {
+                int r0, cnt;
+                mm_group_rows(a.offsets, e, a.P, r0, cnt);
+                const int d = (int)blockIdx.y - r0;
+                if (d >= 0 && d < cnt && d % 16 == 0) {
+                    // (overlapping ranges of corrupt offsets: any of them)
+                    found[0] = 1;
+                    found[1] = e;
+                    found[2] = blockIdx.y;
+                    found[3] = min(16, cnt - d);
+                }
             }
         }
         __syncthreads();
-        if (!found[2]) return;
-        group = __builtin_amdgcn_readfirstlane(found[0]);
-        n = __builtin_amdgcn_readfirstlane(found[1]);
+        if (!found[0]) return;
+        group = __builtin_amdgcn_readfirstlane(found[1]);
+        row0 = __builtin_amdgcn_readfirstlane(found[2]);
+        n = min(__builtin_amdgcn_readfirstlane(found[3]), a.P - row0);
     } else {
         row0 = 16 * blockIdx.y;
         n = min(16, a.P - row0);
     }
-    n = min(n, a.P - row0);
 
     // this wave's weight rows and share of the contraction
     const int ng = W8_WAVES / kw, kpart = w % kw;
@@ -176,24 +199,28 @@ int w8_kw(int K) {
 template <typename T>
 hipError_t w8_run(const M8Args& a, hipStream_t s) {
     const int kw = w8_kw(a.K), ng = W8_WAVES / kw;
-    const uint32_t gy = a.offsets ? (uint32_t)a.P : (uint32_t)((a.P + 15) / 16);
+    // grouped: a workgroup row per chunk that there can be, or per row where that is fewer
+    const int most = a.P / 16 + (a.E < a.P ? a.E : a.P), scan = most < a.P;
+    const uint32_t gy = !a.offsets ? (uint32_t)((a.P + 15) / 16) : (uint32_t)(scan ? most : a.P);
     const bool glu = a.act == MM_SWIGLU;
     // two row tiles per wave once there are 4 workgroups per CU with them
-    const bool two = glu || (int64_t)((a.N + 31) / 32) * (a.offsets ? a.P : 1) >= 1024 * ng;
+    const bool two = glu || (int64_t)((a.N + 31) / 32) * (a.offsets ? gy : 1) >= 1024 * ng;
     const int per = glu ? 16 : (two ? 32 : 16), cols = glu ? a.N / 2 : a.N;
     const dim3 g((uint32_t)((cols + per * ng - 1) / (per * ng)), gy);
     if (glu)
-        w8_kernel<T, 2, true><<<g, 64 * W8_WAVES, 0, s>>>(a, kw);
+        w8_kernel<T, 2, true><<<g, 64 * W8_WAVES, 0, s>>>(a, kw, scan);
     else if (two)
-        w8_kernel<T, 2, false><<<g, 64 * W8_WAVES, 0, s>>>(a, kw);
+        w8_kernel<T, 2, false><<<g, 64 * W8_WAVES, 0, s>>>(a, kw, scan);
     else
-        w8_kernel<T, 1, false><<<g, 64 * W8_WAVES, 0, s>>>(a, kw);
+        w8_kernel<T, 1, false><<<g, 64 * W8_WAVES, 0, s>>>(a, kw, scan);
     return hipGetLastError();
 }
 
 }  // namespace
 
-bool m8_rows_takes(int P, int N, int E) {
+bool m8_rows_takes(int P, int K, int N, int E) {
+    const double chunks = P / 16.0 + (E == 1 ? 0.5 : (E < P ? E : P) / 2.0);   // about
+    if (chunks * N * K <= (double)W8_REREAD) return true;
     if (E > 1) return P <= 16 || (P <= 256 && P <= 2 * E);
     return P <= 8 || (P <= 16 && N < 32768);
 }

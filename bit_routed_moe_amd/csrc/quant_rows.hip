@@ -154,6 +154,8 @@ hipError_t qr_run(int rows, int K, const T* x, int64_t ldx, int8_t* codes, int64
     const int chunks = (K + QrVec<T>::N - 1) / QrVec<T>::N;
     if (chunks <= 4 * 64)   // a wave holds the row
         qr_kernel<T, 1><<<(uint32_t)((rows + 3) / 4), 256, 0, s>>>(rows, K, x, ldx, codes, ldq, scale);
+    else if (rows <= 256)   // fewer rows than CUs: 16 waves each
+        qr_kernel<T, 16><<<(uint32_t)rows, 1024, 0, s>>>(rows, K, x, ldx, codes, ldq, scale);
     else
         qr_kernel<T, 4><<<(uint32_t)rows, 256, 0, s>>>(rows, K, x, ldx, codes, ldq, scale);
     return hipGetLastError();
