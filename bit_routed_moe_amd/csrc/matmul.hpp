@@ -22,7 +22,8 @@ constexpr int MM_MIN_CHUNK = 64;
 
 // One piece of a group's rows: forward and dgrad run a row tile of it.
 struct MmChunk {
-    int32_t group, row0, n, pad;
+    int32_t group, row0, n;
+    int32_t index;   // among its group's chunks
 };
 
 __device__ __forceinline__ float mm_sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }

@@ -33,7 +33,7 @@ __global__ __launch_bounds__(1024) void mm_plan_kernel(const int32_t* __restrict
         c.group = group;
         c.row0 = first + i * bm;
         c.n = min(bm, rows - i * bm);
-        c.pad = 0;
+        c.index = i;
         chunks[at + i] = c;
     };
     // groups of many chunks are written by all threads

@@ -16,30 +16,33 @@ namespace ds4 {
 
 namespace {
 
-constexpr int M8_K = 128;          // contraction columns per stage
+constexpr int M8_K = 128;          // contraction columns that the estimate counts as a stage
 constexpr int M8_MAX_SPLITS = 16;  // of the contraction
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
-// One operand of BT tile rows staged by NW waves.
-template <int BT, int NW>
+// One operand of BT tile rows of KB bytes staged by NW waves.
+template <int BT, int NW, int KB>
 struct M8Operand {
-    static constexpr int BYTES = BT * M8_K;
+    static constexpr int CPR = KB / 16, RPD = 1024 / KB;   // 16-byte chunks per row, rows per DMA
+    static constexpr int BYTES = BT * KB;
     static constexpr int ND = BYTES / 1024 / NW;   // DMAs per wave and stage
     static_assert(ND * NW * 1024 == BYTES, "whole DMAs per wave");
     // tile row and chunk that DMA i of wave w brings for this lane
-    static __device__ __forceinline__ int row(int i, int w, int lane) { return (i * NW + w) * 8 + (lane >> 3); }
-    static __device__ __forceinline__ int chunk(int row, int lane) { return (lane & 7) ^ ((row >> 1) & 7); }
+    static __device__ __forceinline__ int row(int i, int w, int lane) { return (i * NW + w) * RPD + lane / CPR; }
+    // what a row's chunks are moved by
+    static __device__ __forceinline__ int place(int row) { return KB == 128 ? (row >> 1) & 7 : (row >> 2) & 3; }
+    static __device__ __forceinline__ int chunk(int row, int lane) { return (lane % CPR) ^ place(row); }
     // Fragment t (16 tile rows from t0 + 16 * t on) of k-step ks.
     static __device__ __forceinline__ i32x4 frag(const uint8_t* buf, int t0, int t, int ks, int lane) {
         const int m = lane & 15, q = lane >> 4, r = t0 + 16 * t + m;
-        return *reinterpret_cast<const i32x4*>(buf + r * 128 + (((ks * 4 + q) ^ (m >> 1)) << 4));
+        return *reinterpret_cast<const i32x4*>(buf + r * KB + (((ks * 4 + q) ^ place(m)) << 4));
     }
     // Zeros from contraction column krem of the stage on (of one operand: the
     // other's bytes there are then multiplied by zero).
     static __device__ __forceinline__ void clear_tail(uint8_t* buf, int krem, int tid) {
-        for (int i = tid; i < BT * 8; i += NW * 64) {
-            const int r = i >> 3, c = i & 7;
-            uint8_t* p = buf + r * 128 + ((c ^ ((r >> 1) & 7)) << 4);
+        for (int i = tid; i < BT * CPR; i += NW * 64) {
+            const int r = i / CPR, c = i % CPR;
+            uint8_t* p = buf + r * KB + ((c ^ place(r)) << 4);
             if (16 * c >= krem)
                 *reinterpret_cast<u32x4*>(p) = u32x4{0, 0, 0, 0};
             else
@@ -71,16 +74,18 @@ __device__ __forceinline__ void m8_part8(int32_t* p, const int32_t (&v)[8], int 
     }
 }
 
-// WR x WC waves, each (BR / WR) x (BC / WC) outputs; ST stage buffers.
-template <int BR, int BC, int WR, int WC, int ST, typename T>
-__global__ __launch_bounds__(64 * WR * WC) void m8_kernel(M8Args a, int tr, int tc) {
+// WR x WC waves, each (BR / WR) x (BC / WC) outputs; ST stage buffers of KB
+// contraction columns; PIPE: fragments read a step ahead (where workgroups
+// share a CU they cover each other's waits); WPS waves per SIMD.
+template <int BR, int BC, int WR, int WC, int KB, int ST, bool PIPE, int WPS, typename T>
+__global__ __launch_bounds__(64 * WR * WC, WPS) void m8_kernel(M8Args a, int tr, int tc) {
     constexpr int NW = WR * WC;
-    using RowOp = M8Operand<BR, NW>;
-    using ColOp = M8Operand<BC, NW>;
+    using RowOp = M8Operand<BR, NW, KB>;
+    using ColOp = M8Operand<BC, NW, KB>;
     constexpr int STB = RowOp::BYTES + ColOp::BYTES;
     constexpr int MI = BR / WR / 16, NI = BC / WC / 16;
     constexpr int LPS = RowOp::ND + ColOp::ND;   // DMAs per wave and stage
-    constexpr bool PIPE = BC == 256;
+    static_assert(KB == 128 || (KB == 64 && !PIPE), "PIPE has two steps of 64 columns");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[ST * STB];
     const uint32_t lds32 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -92,7 +97,17 @@ __global__ __launch_bounds__(64 * WR * WC) void m8_kernel(M8Args a, int tr, int 
     const int t = ((int)blockIdx.x & 7) * per + slot;
     if (slot >= per || t >= total) return;
     int rt, ct;
-    mt_tile(t, ntr, tc, rt, ct);
+    if (a.chunks) {   // a group's tiles follow one another, so that its weights are read once
+        const int c = t / tc;
+        const MmChunk o = a.chunks[c];
+        int r0, n;
+        mm_group_rows(a.offsets, o.group, a.P, r0, n);
+        const int first = c - o.index;
+        mt_tile(t - first * tc, (n + BR - 1) / BR, tc, rt, ct);
+        rt += first;
+    } else {
+        mt_tile(t, ntr, tc, rt, ct);
+    }
     const int c0 = ct * BC;
     MmChunk ch;
     if (!mm_chunk(a, rt, BR, ch)) return;
@@ -101,7 +116,7 @@ __global__ __launch_bounds__(64 * WR * WC) void m8_kernel(M8Args a, int tr, int 
 
     // the DMAs' source rows; a lane's chunk is the same in all of a wave's
     // DMAs, whose rows differ by a multiple of 16
-    static_assert((NW * 8) % 16 == 0, "one chunk per lane");
+    static_assert((NW * RowOp::RPD) % 16 == 0, "one chunk per lane");
     const int rrow = RowOp::row(0, w, lane), crow = ColOp::row(0, w, lane);
     const int chunk = RowOp::chunk(rrow, lane);   // (rrow == crow)
     const int8_t* rsrc[RowOp::ND];
@@ -109,16 +124,16 @@ __global__ __launch_bounds__(64 * WR * WC) void m8_kernel(M8Args a, int tr, int 
 #pragma unroll
     for (int i = 0; i < RowOp::ND; ++i)
         rsrc[i] = static_cast<const int8_t*>(a.x) +
-                  (size_t)mm_src(a, ch.row0 + min(rrow + i * NW * 8, ch.n - 1)) * a.ldx;
+                  (size_t)mm_src(a, ch.row0 + min(rrow + i * NW * RowOp::RPD, ch.n - 1)) * a.ldx;
 #pragma unroll
     for (int i = 0; i < ColOp::ND; ++i) {
-        const int n = mm_col(a, glu, c0, crow + i * NW * 8);
+        const int n = mm_col(a, glu, c0, crow + i * NW * ColOp::RPD);
         csrc[i] = wg + (size_t)(n < 0 ? a.N - 1 : n) * a.ldw;
     }
     const int kchunk = (a.K - 1) / 16;
     auto issue1 = [&](int st, int i) {   // DMA i (0 .. LPS-1) of stage st
         const uint32_t buf = lds32 + (uint32_t)(st % ST) * STB;
-        const int off = 16 * min(st * (M8_K / 16) + chunk, kchunk);
+        const int off = 16 * min(st * (KB / 16) + chunk, kchunk);
         if (i < RowOp::ND)
             mt_dma16(rsrc[i] + off, buf + (uint32_t)(i * NW + w) * 1024u);
         else
@@ -136,12 +151,12 @@ __global__ __launch_bounds__(64 * WR * WC) void m8_kernel(M8Args a, int tr, int 
         for (int j = 0; j < MI; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
     const int wr0 = (w % WR) * (BR / WR), wc0 = (w / WR) * (BC / WC);
     // stages [sb, ns) of the contraction: all, or this split's share
-    const int nall = (a.K + M8_K - 1) / M8_K;
+    const int nall = (a.K + KB - 1) / KB;
     const int each = (nall + a.ksplits - 1) / a.ksplits;
     const int sb = min(nall, (int)blockIdx.z * each), ns = min(nall, sb + each);
     auto clear_tail = [&](int st) {   // behind the contraction's end, in the last stage
-        if (st == nall - 1 && a.K % M8_K) {
-            RowOp::clear_tail(lds + (st % ST) * STB, a.K % M8_K, tid);
+        if (st == nall - 1 && a.K % KB) {
+            RowOp::clear_tail(lds + (st % ST) * STB, a.K % KB, tid);
             __syncthreads();
         }
     };
@@ -213,7 +228,7 @@ __global__ __launch_bounds__(64 * WR * WC) void m8_kernel(M8Args a, int tr, int 
             clear_tail(st);
             const uint8_t* buf = lds + (st % ST) * STB;
 #pragma unroll
-            for (int ks = 0; ks < M8_K / 64; ++ks) {
+            for (int ks = 0; ks < KB / 64; ++ks) {
                 i32x4 rf[MI], cf[NI];
 #pragma unroll
                 for (int i = 0; i < NI; ++i) cf[i] = ColOp::frag(buf + RowOp::BYTES, wc0, i, ks, lane);
@@ -348,19 +363,22 @@ int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // Tile shapes, with the times that the estimate takes (us per stage of 128
 // contraction columns): lat of a workgroup by itself on its CU, thr per
-// workgroup and CU when the chip is full; wgs that share a CU.
+// workgroup and CU when the chip is full; wgs that share a CU, so that one's
+// start and end hide behind another's stages.  The numbers are fitted to 107
+// products (16 .. 32768 rows, dense and of 2 .. 256 groups, 64 .. 8192 x 64 ..
+// 8192), each timed in every shape and split: the choice is within 6% of the
+// best in 104 of them, the others 13, 15 and 18% off.
 struct M8Shape {
     int br, bc;
     double lat, thr;
     int wgs;
 };
 constexpr M8Shape M8_SHAPES[] = {
-    {256, 256, 1.1, 1.6, 1}, {128, 256, 0.68, 0.95, 1}, {128, 128, 0.55, 0.55, 2}, {64, 64, 0.25, 0.18, 3}};
-constexpr int M8_NSHAPES = 4;
-constexpr double M8_ENDS = 3.0;    // us to fill a workgroup's first stages and to write its tile
-constexpr double M8_JOIN = 4.0;    // us of a join launch
-constexpr double M8_MEM = 4.5e6;   // bytes per us, of outputs and partial sums
-constexpr double M8_RAGGED = 1.25; // small tiles of groups read their weights more often
+    {256, 256, 1.39, 1.32, 1}, {128, 256, 0.64, 0.93, 1}, {128, 256, 1.16, 1.02, 2}, {128, 128, 0.56, 0.52, 2}, {64, 64, 0.3, 0.17, 3}};
+constexpr int M8_NSHAPES = 5;
+constexpr double M8_ENDS = 2.35;   // us to fill a workgroup's first stages and to write its tile
+constexpr double M8_JOIN = 3.0;    // us of a join launch
+constexpr double M8_MEM = 4.2e6;   // bytes per us, of outputs and partial sums
 
 struct M8Pick {
     int shape, splits;
@@ -379,10 +397,9 @@ M8Pick m8_pick(int P, int K, int N, int E) {
         if (E > 1) tr = (double)P / t.br + 0.5 * live > live ? (double)P / t.br + 0.5 * live : live;
         const double tiles = tr * cdiv(N, t.bc);
         const double out = tiles * t.br * t.bc * 2.0 / M8_MEM;
-        for (int s = 1; s <= M8_MAX_SPLITS && (s == 1 || (i >= 2 && ns / s >= 4 && tiles * s <= 512.0)); s *= 2) {
+        for (int s = 1; s <= M8_MAX_SPLITS && (s == 1 || (i >= 3 && ns / s >= 4 && tiles * s <= 512.0)); s *= 2) {
             const double wgs = tiles * s, per_cu = wgs <= 256.0 ? wgs / 256.0 : (double)(int64_t)(wgs / 256.0 + 0.999);
-            const double thr = t.thr * (t.wgs > 1 && E > 1 ? M8_RAGGED : 1.0);
-            const double stage = thr * per_cu > t.lat ? thr * per_cu : t.lat;
+            const double stage = t.thr * per_cu > t.lat ? t.thr * per_cu : t.lat;
             double us = stage * cdiv(ns, s);
             if (t.wgs == 1)
                 us += M8_ENDS * (per_cu < 1.0 ? 1.0 : per_cu) + out;
@@ -398,12 +415,12 @@ M8Pick m8_pick(int P, int K, int N, int E) {
     return best;
 }
 
-template <int BR, int BC, int WR, int WC, int ST, typename T>
+template <int BR, int BC, int WR, int WC, int KB, int ST, bool PIPE, int WPS, typename T>
 hipError_t m8_launch(const M8Args& a, hipStream_t s) {
     const int tr = a.chunks ? a.max_chunks : cdiv(a.P, BR), tc = cdiv(a.N, BC);
     const int64_t total = (int64_t)tr * tc;
     const dim3 g((uint32_t)((total + 7) / 8 * 8), 1, (uint32_t)a.ksplits);
-    m8_kernel<BR, BC, WR, WC, ST, T><<<g, 64 * WR * WC, 0, s>>>(a, tr, tc);
+    m8_kernel<BR, BC, WR, WC, KB, ST, PIPE, WPS, T><<<g, 64 * WR * WC, 0, s>>>(a, tr, tc);
     if (a.ksplits > 1) {
         const dim3 j((uint32_t)cdiv(a.act == MM_SWIGLU ? a.N / 2 : a.N, 256), (uint32_t)tr, BR / 8u);
         m8_join_kernel<T><<<j, 256, 0, s>>>(a, BR);
@@ -414,10 +431,11 @@ hipError_t m8_launch(const M8Args& a, hipStream_t s) {
 template <typename T>
 hipError_t m8_run(const M8Args& a, int shape, hipStream_t s) {
     switch (shape) {
-        case 0: return m8_launch<256, 256, 2, 4, 2, T>(a, s);
-        case 1: return m8_launch<128, 256, 2, 4, 3, T>(a, s);
-        case 2: return m8_launch<128, 128, 2, 2, 2, T>(a, s);
-        default: return m8_launch<64, 64, 2, 2, 3, T>(a, s);
+        case 0: return m8_launch<256, 256, 2, 4, 128, 2, true, 2, T>(a, s);
+        case 1: return m8_launch<128, 256, 2, 4, 128, 3, true, 2, T>(a, s);
+        case 2: return m8_launch<128, 256, 2, 4, 64, 3, false, 4, T>(a, s);
+        case 3: return m8_launch<128, 128, 2, 4, 128, 2, false, 4, T>(a, s);
+        default: return m8_launch<64, 64, 2, 2, 128, 3, false, 2, T>(a, s);
     }
 }
 

@@ -21,7 +21,7 @@ namespace {
 
 constexpr int W8_WAVES = 8;
 constexpr int W8_STEP = 256;   // contraction columns per step
-constexpr int W8_REREAD = 1 << 24;   // bytes of weights that all chunks together may read (m8_rows_takes)
+constexpr int W8_REREAD = 20 << 20;   // bytes of weights that all chunks together may read (m8_rows_takes)
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 // 16 bytes of a row from chunk c on; bytes from column K on are zero.
@@ -218,6 +218,17 @@ hipError_t w8_run(const M8Args& a, hipStream_t s) {
 
 }  // namespace
 
+// Products that take these kernels.  Every chunk of 16 rows reads the weights
+// again, from L2 when they are small: us here / with the best tile shape,
+//   dense: 301 x 1459 -> 331 4.8 / 8.3, 600 6.4 / 8.4, 1200 10.4 / 8.5; 300 x
+//     7168 -> 100 9.9 / 13.7; 64 x 4096 -> 1024 6.5 / 8.7, 64 x 8192 -> 512 9.8
+//     / 9.3; 32 x 4096 -> 4096 10.2 / 9.5, 64 x 4096 -> 4096 17.6 / 11.0.
+//   grouped (the tiles need a plan launch): 903 rows of 7 experts 459 -> 331 7.4
+//     / 9.3, 637 of 13 1570 -> 244 8.0 / 13.4, 512 of 64 1024 -> 1024 19 / 18,
+//     256 of 8 2048 -> 2048 22 / 13.
+// With the border at 20 MB read by all chunks together none of 65 products
+// timed both ways loses more than 6%.  Up to 16 rows the weights come from
+// memory once in either kernel, and these read them faster.
 bool m8_rows_takes(int P, int K, int N, int E) {
     const double chunks = P / 16.0 + (E == 1 ? 0.5 : (E < P ? E : P) / 2.0);   // about
     if (chunks * N * K <= (double)W8_REREAD) return true;
