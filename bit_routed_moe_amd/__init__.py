@@ -147,6 +147,28 @@ def _load():
 lib = _load()
 
 
+_SWIGLU = ACT["swiglu"]
+
+
+def _types():
+    import torch
+    return torch.float32, torch.bfloat16, torch.int32, torch.int8
+
+
+_F32, _BF16, _I32, _I8 = _types()
+
+
+def _lookups():
+    """torch's own shortcuts to a device's current stream and to the current
+    device's index (host time of every call: 0.1 us each in place of 1.4 and
+    0.4), None where this torch has none."""
+    import torch
+    return getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+
+
+_raw_stream, _get_device = _lookups()
+
+
 def status_string(st: int) -> str:
     return lib.ds4moe_status_string(st).decode()
 
@@ -169,6 +191,8 @@ def _s(stream, dev=None):
     if stream is not None:
         return ctypes.c_void_p(stream if isinstance(stream, int) else stream.cuda_stream)
     import torch
+    if dev is not None and _raw_stream is not None:
+        return _raw_stream(dev)
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
@@ -288,7 +312,9 @@ def _here():
     """Index of the current HIP device, None without one."""
     import torch
     cuda = torch.cuda
-    return cuda.current_device() if cuda.is_initialized() or cuda.is_available() else None
+    if cuda.is_initialized():
+        return _get_device() if _get_device is not None else cuda.current_device()
+    return cuda.current_device() if cuda.is_available() else None
 
 
 def _vector(name, t, dtype, n, dev):
@@ -443,44 +469,47 @@ def matmul_int8_workspace_bytes(m: MatmulInt8, rows: int) -> int:
     return int(lib.ds4moe_matmul_int8_workspace_bytes(ctypes.byref(m), rows))
 
 
-def _row_stride(t, cols):
-    """Elements between the rows of a matrix (`cols`, where there is one row)."""
-    return t.stride(-2) if t.dim() > 1 and t.shape[-2] > 1 else cols
+def _own_rows(name, t, dtype, rows, cols, q, dev):
+    """Device pointer and row stride of a matrix whose stride is its own: `rows`
+    rows of `cols` elements.  (A single row has no stride to be off: the least
+    multiple of q.)"""
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 2 and rows > 1 and shape[0] >= rows and shape[1] >= cols and strides[1] == 1 and t.dtype is dtype:
+        if t.get_device() != dev:
+            raise Ds4MoeError(-1, f"{name} on {t.device}, not on the current HIP device {dev}")
+        return t.data_ptr(), strides[0]
+    ld = -(-cols // q) * q if rows == 1 else strides[-2] if len(shape) > 1 and shape[-2] > 1 else cols
+    return _matrix(name, t, dtype, rows, cols, ld, dev), ld
 
 
 def quantize_rows_int8(rows, cols, x, codes, scale, stream=None):
     """codes [rows][cols] (int8) and scale [rows] (fp32) of the rows of x (fp32 or
     bf16); rows of x and codes may be any multiple of 16 bytes apart."""
-    import torch
-    f32, dev = torch.float32, _here()
-    if x.dtype not in (f32, torch.bfloat16):
-        raise Ds4MoeError(-1, f"x is {x.dtype}, not {f32} or {torch.bfloat16}")
-    ldx, ldq = _row_stride(x, cols), _row_stride(codes, cols)
-    if rows == 1:    # (a single row has no stride to be off)
-        ldx, ldq = -(-cols // 8) * 8, -(-cols // 16) * 16
-    _check(lib.ds4moe_quantize_rows_int8(
-        rows, cols, int(x.dtype != f32), _matrix("x", x, x.dtype, rows, cols, ldx, dev), ldx,
-        _matrix("codes", codes, torch.int8, rows, cols, ldq, dev), ldq, _vector("scale", scale, f32, rows, dev),
-        _s(stream, dev)))
+    dev, t = _here(), x.dtype
+    if t is not _F32 and t is not _BF16:
+        raise Ds4MoeError(-1, f"x is {t}, not {_F32} or {_BF16}")
+    xp, ldx = _own_rows("x", x, t, rows, cols, 8, dev)
+    cp, ldq = _own_rows("codes", codes, _I8, rows, cols, 16, dev)
+    _check(lib.ds4moe_quantize_rows_int8(rows, cols, 0 if t is _F32 else 1, xp, ldx, cp, ldq,
+                                         _vector("scale", scale, _F32, rows, dev), _s(stream, dev)))
 
 
 def _m8_plan(m):
-    """As _mm_plan, without the gradients' type."""
-    import torch
-    types = (torch.float32, torch.bfloat16)
-    return (types[m.dtype] if 0 <= m.dtype <= 1 else None, torch.int8, torch.float32, m.groups * m.out_dim,
-            m.out_dim // 2 if m.act == ACT["swiglu"] else m.out_dim, _here())
+    """Type of a descriptor's bias and rows of y, rows of w, columns of y, and
+    the current device."""
+    dt, n = m.dtype, m.out_dim
+    return (_F32 if dt == 0 else _BF16 if dt == 1 else None, m.groups * n, n // 2 if m.act == _SWIGLU else n, _here())
 
 
 def linear_int8(m, rows, x, x_scale, w, w_scale, y, bias=None, residual=None, workspace=None, stream=None):
     """y = act((x W^T) x_scale w_scale + bias) + residual on int8 codes x and w
     with an fp32 scale for each of their rows."""
-    dt, i8, f32, wrows, oc, dev = _m8_plan(m)
+    dt, wrows, oc, dev = _m8_plan(m)
     k, ldy = m.in_dim, m.ldy
     ws, nws = _workspace(workspace, dev)
     _check(lib.ds4moe_linear_int8(
-        ctypes.byref(m), rows, _matrix("x", x, i8, rows, k, m.ldx, dev), _vector("x_scale", x_scale, f32, rows, dev),
-        _matrix("w", w, i8, wrows, k, m.ldw, dev), _vector("w_scale", w_scale, f32, wrows, dev),
+        ctypes.byref(m), rows, _matrix("x", x, _I8, rows, k, m.ldx, dev), _vector("x_scale", x_scale, _F32, rows, dev),
+        _matrix("w", w, _I8, wrows, k, m.ldw, dev), _vector("w_scale", w_scale, _F32, wrows, dev),
         _vector("bias", bias, dt, wrows, dev), _matrix("residual", residual, dt, rows, oc, ldy, dev),
         _matrix("y", y, dt, rows, oc, ldy, dev), ws, nws, _s(stream, dev)))
 
@@ -489,15 +518,14 @@ def grouped_matmul_int8(m, rows, x, x_scale, w, w_scale, expert_offsets, y, sort
                         bias=None, workspace=None, stream=None):
     """linear_int8 by expert: rows, expert_offsets, sorted_pair, top_k and x_rows
     as in grouped_matmul; x_scale has a scale for each row of x."""
-    import torch
-    dt, i8, f32, wrows, oc, dev = _m8_plan(m)
-    k, xr, i32 = m.in_dim, _x_rows(x, rows) if x_rows is None else x_rows, torch.int32
+    dt, wrows, oc, dev = _m8_plan(m)
+    k, xr = m.in_dim, _x_rows(x, rows) if x_rows is None else x_rows
     ws, nws = _workspace(workspace, dev)
     _check(lib.ds4moe_grouped_matmul_int8(
-        ctypes.byref(m), rows, _matrix("x", x, i8, xr, k, m.ldx, dev), _vector("x_scale", x_scale, f32, xr, dev), xr,
-        _matrix("w", w, i8, wrows, k, m.ldw, dev), _vector("w_scale", w_scale, f32, wrows, dev),
-        _vector("bias", bias, dt, wrows, dev), _vector("expert_offsets", expert_offsets, i32, m.groups + 1, dev),
-        _vector("sorted_pair", sorted_pair, i32, rows, dev), top_k, _matrix("y", y, dt, rows, oc, m.ldy, dev), ws, nws,
+        ctypes.byref(m), rows, _matrix("x", x, _I8, xr, k, m.ldx, dev), _vector("x_scale", x_scale, _F32, xr, dev), xr,
+        _matrix("w", w, _I8, wrows, k, m.ldw, dev), _vector("w_scale", w_scale, _F32, wrows, dev),
+        _vector("bias", bias, dt, wrows, dev), _vector("expert_offsets", expert_offsets, _I32, m.groups + 1, dev),
+        _vector("sorted_pair", sorted_pair, _I32, rows, dev), top_k, _matrix("y", y, dt, rows, oc, m.ldy, dev), ws, nws,
         _s(stream, dev)))
 
 
@@ -511,83 +539,79 @@ def make_rows(hidden, top_k, dtype="bf16", ldx=0, ldr=0) -> Rows:
 
 
 def _rows_plan(d, T):
-    """Type of a descriptor's rows, fp32, int32, pairs, and the current device."""
-    import torch
-    return ((torch.float32, torch.bfloat16)[d.dtype] if 0 <= d.dtype <= 1 else None, torch.float32, torch.int32,
-            T * d.top_k, _here())
+    """Type of a descriptor's rows, pairs, and the current device."""
+    dt = d.dtype
+    return _F32 if dt == 0 else _BF16 if dt == 1 else None, T * d.top_k, _here()
 
 
 def dispatch(d, T, rows, x, pair_pos, out, topk_w=None, sorted_pair=None, stream=None):
     """out[pair_pos[t, j]] = topk_w[t, j] * x[t] (weight 1 without topk_w); pairs
     whose position is outside [0, rows) are dropped.  With sorted_pair, rows
     whose entry is no pair are set to zero."""
-    dt, f32, i32, n, dev = _rows_plan(d, T)
+    dt, n, dev = _rows_plan(d, T)
     _check(lib.ds4moe_dispatch(
         ctypes.byref(d), T, rows, _matrix("x", x, dt, T, d.hidden, d.ldx, dev),
-        _vector("pair_pos", pair_pos, i32, n, dev), _vector("topk_w", topk_w, f32, n, dev),
-        _vector("sorted_pair", sorted_pair, i32, rows, dev), _matrix("out", out, dt, rows, d.hidden, d.ldr, dev),
+        _vector("pair_pos", pair_pos, _I32, n, dev), _vector("topk_w", topk_w, _F32, n, dev),
+        _vector("sorted_pair", sorted_pair, _I32, rows, dev), _matrix("out", out, dt, rows, d.hidden, d.ldr, dev),
         _s(stream, dev)))
 
 
 def collect(d, T, rows, expert_rows, pair_pos, y, topk_w=None, base=None, stream=None):
     """y[t] = base[t] + sum_j topk_w[t, j] * expert_rows[pair_pos[t, j]]."""
-    dt, f32, i32, n, dev = _rows_plan(d, T)
+    dt, n, dev = _rows_plan(d, T)
     _check(lib.ds4moe_collect(
         ctypes.byref(d), T, rows, _matrix("expert_rows", expert_rows, dt, rows, d.hidden, d.ldr, dev),
-        _vector("pair_pos", pair_pos, i32, n, dev), _vector("topk_w", topk_w, f32, n, dev),
+        _vector("pair_pos", pair_pos, _I32, n, dev), _vector("topk_w", topk_w, _F32, n, dev),
         _matrix("base", base, dt, T, d.hidden, d.ldx, dev), _matrix("y", y, dt, T, d.hidden, d.ldx, dev),
         _s(stream, dev)))
 
 
 def dispatch_backward(d, T, rows, dout, pair_pos, topk_w=None, x=None, dx=None, dtopk_w=None, stream=None):
     """Gradients of dispatch: dx, dtopk_w, or both (x is read for dtopk_w only)."""
-    dt, f32, i32, n, dev = _rows_plan(d, T)
+    dt, n, dev = _rows_plan(d, T)
     x = None if dtopk_w is None else x
     _check(lib.ds4moe_dispatch_backward(
         ctypes.byref(d), T, rows, _matrix("x", x, dt, T, d.hidden, d.ldx, dev),
-        _matrix("dout", dout, dt, rows, d.hidden, d.ldr, dev), _vector("pair_pos", pair_pos, i32, n, dev),
-        _vector("topk_w", topk_w, f32, n, dev), _matrix("dx", dx, dt, T, d.hidden, d.ldx, dev),
-        _vector("dtopk_w", dtopk_w, f32, n, dev), _s(stream, dev)))
+        _matrix("dout", dout, dt, rows, d.hidden, d.ldr, dev), _vector("pair_pos", pair_pos, _I32, n, dev),
+        _vector("topk_w", topk_w, _F32, n, dev), _matrix("dx", dx, dt, T, d.hidden, d.ldx, dev),
+        _vector("dtopk_w", dtopk_w, _F32, n, dev), _s(stream, dev)))
 
 
 def collect_backward(d, T, rows, dy, pair_pos, expert_rows=None, topk_w=None, sorted_pair=None, drows=None,
                      dtopk_w=None, stream=None):
     """Gradients of collect: drows, dtopk_w, or both (expert_rows is read for
     dtopk_w only); sorted_pair as in dispatch."""
-    dt, f32, i32, n, dev = _rows_plan(d, T)
+    dt, n, dev = _rows_plan(d, T)
     expert_rows = None if dtopk_w is None else expert_rows
     _check(lib.ds4moe_collect_backward(
         ctypes.byref(d), T, rows, _matrix("expert_rows", expert_rows, dt, rows, d.hidden, d.ldr, dev),
-        _matrix("dy", dy, dt, T, d.hidden, d.ldx, dev), _vector("pair_pos", pair_pos, i32, n, dev),
-        _vector("topk_w", topk_w, f32, n, dev), _vector("sorted_pair", sorted_pair, i32, rows, dev),
-        _matrix("drows", drows, dt, rows, d.hidden, d.ldr, dev), _vector("dtopk_w", dtopk_w, f32, n, dev),
+        _matrix("dy", dy, dt, T, d.hidden, d.ldx, dev), _vector("pair_pos", pair_pos, _I32, n, dev),
+        _vector("topk_w", topk_w, _F32, n, dev), _vector("sorted_pair", sorted_pair, _I32, rows, dev),
+        _matrix("drows", drows, dt, rows, d.hidden, d.ldr, dev), _vector("dtopk_w", dtopk_w, _F32, n, dev),
         _s(stream, dev)))
 
 
 def route_backward(cfg, T, topk_idx, topk_w, dtopk_w, dlogits, stream=None):
     """dlogits [T, n_experts] of route from the gradient of its weights."""
-    import torch
-    f32, dev = torch.float32, _here()
-    n = T * cfg.top_k
+    n, dev = T * cfg.top_k, _here()
     _check(lib.ds4moe_route_backward(
-        ctypes.byref(cfg), T, _vector("topk_idx", topk_idx, torch.int32, n, dev),
-        _vector("topk_w", topk_w, f32, n, dev), _vector("dtopk_w", dtopk_w, f32, n, dev),
-        _vector("dlogits", dlogits, f32, T * cfg.n_experts, dev), _s(stream, dev)))
+        ctypes.byref(cfg), T, _vector("topk_idx", topk_idx, _I32, n, dev),
+        _vector("topk_w", topk_w, _F32, n, dev), _vector("dtopk_w", dtopk_w, _F32, n, dev),
+        _vector("dlogits", dlogits, _F32, T * cfg.n_experts, dev), _s(stream, dev)))
 
 
 # ---- rules on logits -----------------------------------------------------------
 
 def _logit_rows(name, t, B, V, dev):
     """Type, row stride and device pointer of B rows of V logits."""
-    import torch
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise Ds4MoeError(-1, f"{name} is {t.dtype}, not torch.float32 or torch.bfloat16")
+    if t.dtype is not _F32 and t.dtype is not _BF16:
+        raise Ds4MoeError(-1, f"{name} is {t.dtype}, not {_F32} or {_BF16}")
     rows = 1 if t.dim() < 2 else t.shape[0]
     if t.dim() not in (1, 2) or rows < B or t.shape[-1] < V or (V > 1 and t.stride(-1) != 1):
         raise Ds4MoeError(-2, f"{name} of shape {tuple(t.shape)}, strides {t.stride()} for {B} rows of {V}")
     if t.get_device() != dev:
         raise Ds4MoeError(-1, f"{name} on {t.device}, not on the current HIP device {dev}")
-    return int(t.dtype == torch.bfloat16), t.stride(0) if B > 1 else V, t.data_ptr()
+    return 1 if t.dtype is _BF16 else 0, t.stride(0) if B > 1 else V, t.data_ptr()
 
 
 def adjust_logits(B, V, logits, out, history=None, history_offsets=None, prompt_len=None, repetition=None,
@@ -600,24 +624,23 @@ def adjust_logits(B, V, logits, out, history=None, history_offsets=None, prompt_
     int32, the others fp32 (repetition, presence, frequency [B], bias_value as
     long as bias_token), all contiguous but for the rows of logits, out and
     mask."""
-    import torch
-    f32, i32, dev = torch.float32, torch.int32, _here()
+    dev = _here()
     dt, ld, src = _logit_rows("logits", logits, B, V, dev)
     odt, ldo, dst = _logit_rows("out", out, B, V, dev)
     nh = 0 if history is None else history.numel()
     nb = 0 if bias_token is None else bias_token.numel()
     # (an empty list is a list all the same; it need not have memory)
     r = LogitRules(
-        _vector("history", history, i32, nh, dev), _vector("history_offsets", history_offsets, i32, B + 1, dev),
-        _vector("prompt_len", prompt_len, i32, B, dev), _vector("repetition", repetition, f32, B, dev),
-        _vector("presence", presence, f32, B, dev), _vector("frequency", frequency, f32, B, dev),
-        _vector("bias_token", bias_token, i32, nb, dev), _vector("bias_value", bias_value, f32, nb, dev),
-        _vector("bias_offsets", bias_offsets, i32, B + 1, dev), None, _vector("mask_row", mask_row, i32, B, dev), 0,
+        _vector("history", history, _I32, nh, dev), _vector("history_offsets", history_offsets, _I32, B + 1, dev),
+        _vector("prompt_len", prompt_len, _I32, B, dev), _vector("repetition", repetition, _F32, B, dev),
+        _vector("presence", presence, _F32, B, dev), _vector("frequency", frequency, _F32, B, dev),
+        _vector("bias_token", bias_token, _I32, nb, dev), _vector("bias_value", bias_value, _F32, nb, dev),
+        _vector("bias_offsets", bias_offsets, _I32, B + 1, dev), None, _vector("mask_row", mask_row, _I32, B, dev), 0,
         nh, nb, 0)
     if mask is not None:
         words = (V + 31) // 32
-        if mask.dtype != i32:
-            raise Ds4MoeError(-1, f"mask is {mask.dtype}, not {i32}")
+        if mask.dtype is not _I32:
+            raise Ds4MoeError(-1, f"mask is {mask.dtype}, not {_I32}")
         if (mask.dim() != 2 or mask.shape[1] < words or (words > 1 and mask.stride(1) != 1) or
                 (mask.shape[0] > 1 and mask.stride(0) < words)):
             raise Ds4MoeError(-2, f"mask of shape {tuple(mask.shape)}, strides {mask.stride()} for {V} tokens")
