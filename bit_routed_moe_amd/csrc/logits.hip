@@ -19,6 +19,7 @@ namespace ds4 {
 
 namespace {
 
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 // 16 bytes of a row that starts anywhere.
 typedef u32x4 lg_f32x4 __attribute__((aligned(4)));
 typedef u32x4 lg_bf16x8 __attribute__((aligned(2)));
@@ -84,16 +85,31 @@ __device__ __forceinline__ void lg_range(const int32_t* offsets, int b, int tota
 
 constexpr uint32_t LG_PROMPT = 0x80000000u;
 
-// NT threads, C pieces of 16 bytes of logits each; TABLE: there is a history
-// or a bias.
-template <typename TI, typename TO, int NT, int C, bool TABLE>
+// NT threads, C pieces of 16 bytes of logits each; HIST, BIAS: rows have a
+// history, a list of biases (LDS for one table only lets twice the workgroups
+// share a CU).
+template <typename TI, typename TO, int NT, int C, bool HIST, bool BIAS>
 __global__ __launch_bounds__(NT) void lg_kernel(LogitArgs a) {
     constexpr int N = LgVec<TI>::N, S = NT * C * N;
-    __shared__ __attribute__((aligned(16))) uint32_t count[TABLE ? S : 4], place[TABLE ? S : 4];
+    __shared__ __attribute__((aligned(16))) uint32_t count[HIST ? S : 4], place[BIAS ? S : 4];
     const int tid = threadIdx.x, b = blockIdx.y, v0 = blockIdx.x * S;
     const TI* const in = static_cast<const TI*>(a.logits) + (size_t)b * a.ld;
     TO* const out = static_cast<TO*>(a.out) + (size_t)b * a.ld_out;
 
+    // where the row's lists lie, and the first of its history
+    int h0 = 0, nh = 0, made = 0, b0 = 0, nb = 0;
+    typedef i32x4 tokens4 __attribute__((aligned(4)));
+    i32x4 said[2];
+    if constexpr (BIAS) lg_range(a.bias_offsets, b, a.n_bias, b0, nb);
+    if constexpr (HIST) {
+        lg_range(a.history_offsets, b, a.n_history, h0, nh);
+        made = a.prompt_len ? a.prompt_len[b] : 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int i = 4 * (j * NT + tid);
+            if (i + 4 <= nh) said[j] = *reinterpret_cast<const tokens4*>(a.history + (size_t)h0 + i);
+        }
+    }
     // the mask's bits of this thread's pieces (all set without a mask)
     uint32_t bits[C];
     const uint32_t* words = nullptr;
@@ -114,38 +130,44 @@ __global__ __launch_bounds__(NT) void lg_kernel(LogitArgs a) {
         if (bits[i] && v + N <= a.V) piece[i] = *reinterpret_cast<const typename LgVec<TI>::Piece*>(in + v);
     }
 
-    int b0 = 0;
-    if constexpr (TABLE) {
+    if constexpr (HIST || BIAS) {
         for (int i = tid; i < S / 4; i += NT) {
-            reinterpret_cast<u32x4*>(count)[i] = u32x4{0, 0, 0, 0};
-            reinterpret_cast<u32x4*>(place)[i] = u32x4{0, 0, 0, 0};
-        }
-        __syncthreads();
-        if (a.history) {
-            int h0, n;
-            lg_range(a.history_offsets, b, a.n_history, h0, n);
-            const int made = a.prompt_len ? a.prompt_len[b] : 0;
-#pragma unroll 4
-            for (int i = tid; i < n; i += NT) {
-                const uint32_t d = (uint32_t)a.history[(size_t)h0 + i] - (uint32_t)v0;
-                if (d < (uint32_t)S) {
-                    if (i >= made)
-                        atomicAdd(&count[d], 1u);
-                    else
-                        atomicOr(&count[d], LG_PROMPT);
-                }
-            }
-        }
-        if (a.bias_token) {
-            int n;
-            lg_range(a.bias_offsets, b, a.n_bias, b0, n);
-            for (int i = tid; i < n; i += NT) {
-                const uint32_t d = (uint32_t)a.bias_token[(size_t)b0 + i] - (uint32_t)v0;
-                if (d < (uint32_t)S) atomicMax(&place[d], (uint32_t)i + 1);
-            }
+            if constexpr (HIST) reinterpret_cast<u32x4*>(count)[i] = u32x4{0, 0, 0, 0};
+            if constexpr (BIAS) reinterpret_cast<u32x4*>(place)[i] = u32x4{0, 0, 0, 0};
         }
         __syncthreads();
     }
+    if constexpr (HIST) {
+        auto note = [&](int i, int token) {   // token i of the history
+            const uint32_t d = (uint32_t)token - (uint32_t)v0;
+            if (d < (uint32_t)S) {
+                if (i >= made)
+                    atomicAdd(&count[d], 1u);
+                else
+                    atomicOr(&count[d], LG_PROMPT);
+            }
+        };
+        auto note4 = [&](int i, i32x4 t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) note(i + e, t[e]);
+        };
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int i = 4 * (j * NT + tid);
+            if (i + 4 <= nh) note4(i, said[j]);
+        }
+#pragma unroll 2
+        for (uint32_t i = 4 * (2 * NT + tid); i + 4 <= (uint32_t)nh; i += 4 * NT)   // (beyond 31 bits at most by a step)
+            note4((int)i, *reinterpret_cast<const tokens4*>(a.history + (size_t)h0 + i));
+        if (tid < (nh & 3)) note((nh & ~3) + tid, a.history[(size_t)h0 + (nh & ~3) + tid]);
+    }
+    if constexpr (BIAS) {
+        for (uint32_t i = tid; i < (uint32_t)nb; i += NT) {
+            const uint32_t d = (uint32_t)a.bias_token[(size_t)b0 + i] - (uint32_t)v0;
+            if (d < (uint32_t)S) atomicMax(&place[d], i + 1);
+        }
+    }
+    if constexpr (HIST || BIAS) __syncthreads();
     const float rep = a.repetition ? a.repetition[b] : 1.0f;
     const float pres = a.presence ? a.presence[b] : 0.0f, freq = a.frequency ? a.frequency[b] : 0.0f;
     // token d of the segment
@@ -165,15 +187,14 @@ __global__ __launch_bounds__(NT) void lg_kernel(LogitArgs a) {
         if (v + N <= a.V) {
             float l[N];
             if (bits[i]) LgVec<TI>::get(piece[i], l);
-            if constexpr (TABLE) {
+            if constexpr (HIST || BIAS) {
                 if (bits[i]) {
-                    uint32_t any = 0;
 #pragma unroll
                     for (int h = 0; h < N / 4; ++h) {
-                        const u32x4 c = reinterpret_cast<const u32x4*>(count + d)[h];
-                        const u32x4 p = reinterpret_cast<const u32x4*>(place + d)[h];
-                        any = c[0] | c[1] | c[2] | c[3] | p[0] | p[1] | p[2] | p[3];
-                        if (any) {
+                        u32x4 c = {0, 0, 0, 0}, p = {0, 0, 0, 0};
+                        if constexpr (HIST) c = reinterpret_cast<const u32x4*>(count + d)[h];
+                        if constexpr (BIAS) p = reinterpret_cast<const u32x4*>(place + d)[h];
+                        if (c[0] | c[1] | c[2] | c[3] | p[0] | p[1] | p[2] | p[3]) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) l[4 * h + e] = rule(l[4 * h + e], c[e], p[e]);
                         }
@@ -186,7 +207,7 @@ __global__ __launch_bounds__(NT) void lg_kernel(LogitArgs a) {
         } else {   // the row's end
             for (int e = 0; v + e < a.V; ++e) {
                 float l = LgVec<TI>::get(in[v + e]);
-                if constexpr (TABLE) l = rule(l, count[d + e], place[d + e]);
+                if constexpr (HIST || BIAS) l = rule(l, HIST ? count[d + e] : 0u, BIAS ? place[d + e] : 0u);
                 lg_store1(out + v + e, (bits[i] >> e) & 1 ? l : -INFINITY);
             }
         }
@@ -197,18 +218,28 @@ template <typename TI, typename TO, int NT, int C>
 hipError_t lg_launch(const LogitArgs& a, hipStream_t s) {
     constexpr int S = NT * C * LgVec<TI>::N;
     const dim3 g((uint32_t)((a.V + S - 1) / S), (uint32_t)a.B);
-    if (a.history || a.bias_token)
-        lg_kernel<TI, TO, NT, C, true><<<g, NT, 0, s>>>(a);
+    if (a.history && a.bias_token)
+        lg_kernel<TI, TO, NT, C, true, true><<<g, NT, 0, s>>>(a);
+    else if (a.history)
+        lg_kernel<TI, TO, NT, C, true, false><<<g, NT, 0, s>>>(a);
+    else if (a.bias_token)
+        lg_kernel<TI, TO, NT, C, false, true><<<g, NT, 0, s>>>(a);
     else
-        lg_kernel<TI, TO, NT, C, false><<<g, NT, 0, s>>>(a);
+        lg_kernel<TI, TO, NT, C, false, false><<<g, NT, 0, s>>>(a);
     return hipGetLastError();
 }
 
+// Segments of 8192 tokens (1024 threads) once there are rows and tokens enough
+// for about two of their workgroups per CU; else short ones, that the row's
+// history is read by more workgroups matters less than idle CUs.  us with 1024
+// threads of 8 tokens / 512 of 8 / 256 of 16 / 1024 of 16: 64 rows of 131072,
+// history and biases of 2000 and 30 each 16.0 / 16.2 / 19.3 / 16.7, histories
+// of 32000 25.8 / 31.7 / - / 25.3; 256 rows of 50003, histories of 700 19.0 /
+// 19.3 / - / 20.4, with biases 21.6 / 22.0 / - / 29.1.
 template <typename TI, typename TO>
 hipError_t lg_run(const LogitArgs& a, hipStream_t s) {
-    constexpr int C = 16 / LgVec<TI>::N;   // pieces that make 16 tokens
-    if ((int64_t)a.B * a.V < (int64_t)1024 * 4096) return lg_launch<TI, TO, 256, 1>(a, s);
-    return lg_launch<TI, TO, 256, C>(a, s);
+    if (a.V <= 4096 || (int64_t)a.B * a.V < (int64_t)512 * 8192) return lg_launch<TI, TO, 256, 1>(a, s);
+    return lg_launch<TI, TO, 1024, 8 / LgVec<TI>::N>(a, s);
 }
 
 }  // namespace
