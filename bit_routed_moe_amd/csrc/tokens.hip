@@ -69,12 +69,16 @@ __device__ __forceinline__ u32x4 tk_load(const T* row, int c, int H) {
     return r;
 }
 
-template <typename T>
+template <bool NT = false, typename T>
 __device__ __forceinline__ void tk_store(T* row, int c, int H, u32x4 r) {
     constexpr int N = TkVec<T>::N;
     const int n = H - c * N;
     if (n >= N) {
-        *reinterpret_cast<u32x4*>(row + (size_t)c * N) = r;
+        u32x4* p = reinterpret_cast<u32x4*>(row + (size_t)c * N);
+        if constexpr (NT)
+            __builtin_nontemporal_store(r, p);
+        else
+            *p = r;
     } else {
         const T* e = reinterpret_cast<const T*>(&r);
 #pragma unroll
@@ -86,7 +90,7 @@ __device__ __forceinline__ void tk_store(T* row, int c, int H, u32x4 r) {
 // One wave per pair, the waves of a workgroup share a token; blockIdx.y: a
 // share of the columns (chunks [y * span, ..), none with DOTS).  Workgroups
 // from T on clear the rows that no pair names, 64 of them per wave.
-template <typename T, bool DOTS>
+template <typename T, bool DOTS, bool NT>
 __global__ __launch_bounds__(512) void tk_rows_kernel(TokenArgs a, int span) {
     using V = TkVec<T>;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
@@ -102,7 +106,7 @@ __global__ __launch_bounds__(512) void tk_rows_kernel(TokenArgs a, int span) {
             const int i = __builtin_ctzll(left);
             left &= left - 1;
             T* row = out + (r0 + i) * a.ldr;
-            for (int c = c0 + lane; c < c1; c += 64) tk_store(row, c, a.H, u32x4{0, 0, 0, 0});
+            for (int c = c0 + lane; c < c1; c += 64) tk_store<NT>(row, c, a.H, u32x4{0, 0, 0, 0});
         }
         return;
     }
@@ -144,7 +148,7 @@ __global__ __launch_bounds__(512) void tk_rows_kernel(TokenArgs a, int span) {
                         for (int i = 0; i < V::N; ++i) v[i] *= wt;
                         x[u] = V::put(v);
                     }
-                    if (out && c + 64 * u < c1) tk_store(row, c + 64 * u, a.H, x[u]);
+                    if (out && c + 64 * u < c1) tk_store<NT>(row, c + 64 * u, a.H, x[u]);
                 }
             }
         }
@@ -155,13 +159,34 @@ __global__ __launch_bounds__(512) void tk_rows_kernel(TokenArgs a, int span) {
     }
 }
 
+// Sums of M values (a power of 2, at most 64) over the wave, together: each
+// step halves the values that a lane holds, so 8 sums take 10 exchanges, not
+// 48.  Value i's sum ends in the lanes whose low bits spell i.
+template <int M>
+__device__ __forceinline__ float tk_sums(float (&v)[M], int lane) {
+    int o = 1;
+#pragma unroll
+    for (int n = M / 2; n >= 1; n >>= 1, o <<= 1) {
+        const bool up = lane & o;
+        // keep the odd values where the lane's bit is set, else the even ones
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float keep = up ? v[2 * i + 1] : v[2 * i], give = up ? v[2 * i] : v[2 * i + 1];
+            v[i] = keep + __shfl_xor(give, o, WAVE);
+        }
+    }
+#pragma unroll
+    for (; o < 64; o <<= 1) v[0] += __shfl_xor(v[0], o, WAVE);
+    return v[0];
+}
+
 // One workgroup per token (and share of the columns, as above), a chunk of
 // columns per thread and turn; the k rows are read 8, 4, 2 or 1 at a time.
 template <typename T, bool DOTS>
-__global__ __launch_bounds__(256) void tk_tokens_kernel(TokenArgs a, int span) {
+__global__ __launch_bounds__(512) void tk_tokens_kernel(TokenArgs a, int span) {
     using V = TkVec<T>;
     __shared__ int pos[64];
-    __shared__ float wt[64], dots[4][64];
+    __shared__ float wt[64], dots[8][64];
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 63, w = tid >> 6, t = blockIdx.x;
     const int chunks = (a.H + V::N - 1) / V::N;
     const int c0 = blockIdx.y * span, c1 = min(chunks, c0 + span);
@@ -173,7 +198,7 @@ __global__ __launch_bounds__(256) void tk_tokens_kernel(TokenArgs a, int span) {
         wt[j] = !there ? 0.0f : (a.topk_w ? a.topk_w[p] : 1.0f);
     }
     if constexpr (DOTS)
-        for (int i = tid; i < 4 * 64; i += nt) (&dots[0][0])[i] = 0.0f;
+        for (int i = tid; i < 8 * 64; i += nt) (&dots[0][0])[i] = 0.0f;
     __syncthreads();
     const T* const src = static_cast<const T*>(a.src);
     const T* const base = a.base ? static_cast<const T*>(a.base) + (size_t)t * a.ldx : nullptr;
@@ -196,22 +221,24 @@ __global__ __launch_bounds__(256) void tk_tokens_kernel(TokenArgs a, int span) {
 #pragma unroll
                 for (int i = 0; i < JB; ++i) r[i] = tk_load(src + (size_t)max(pos[j + i], 0) * a.ldr, c, a.H);
             }
+            float dot[JB];
 #pragma unroll
             for (int i = 0; i < JB; ++i) {
                 const bool there = mine && pos[j + i] >= 0;
                 const float wj = wt[j + i];
                 if (!there) r[i] = u32x4{0, 0, 0, 0};
-                float v[V::N], dot = 0.0f;
+                float v[V::N];
                 V::get(r[i], v);
+                dot[i] = 0.0f;
 #pragma unroll
                 for (int e = 0; e < V::N; ++e) {
                     acc[e] += wj * v[e];
-                    if constexpr (DOTS) dot += x[e] * v[e];
+                    if constexpr (DOTS) dot[i] += x[e] * v[e];
                 }
-                if constexpr (DOTS) {
-                    dot = wave_sum(dot);
-                    if (lane == 0) dots[w][j + i] += dot;
-                }
+            }
+            if constexpr (DOTS) {
+                const float sum = tk_sums<JB>(dot, lane);
+                if (lane < JB) dots[w][j + lane] += sum;
             }
         };
         int j = 0;
@@ -282,26 +309,38 @@ hipError_t launch_tokens_to_rows(const TokenArgs& a, bool f32, hipStream_t s) {
     const uint32_t clear = a.sorted_pair && a.out ? (uint32_t)(((int64_t)a.rows + 64 * nw - 1) / (64 * nw)) : 0u;
     const int span = tk_span(a, chunks);
     const dim3 g((uint32_t)a.T + clear, (uint32_t)((chunks + span - 1) / span));
-    const uint32_t nt = 64 * nw;
-    if (f32) {
-        if (a.dw)
-            tk_rows_kernel<float, true><<<g, nt, 0, s>>>(a, span);
-        else
-            tk_rows_kernel<float, false><<<g, nt, 0, s>>>(a, span);
-    } else {
-        if (a.dw)
-            tk_rows_kernel<uint16_t, true><<<g, nt, 0, s>>>(a, span);
-        else
-            tk_rows_kernel<uint16_t, false><<<g, nt, 0, s>>>(a, span);
-    }
+    // Rows that do not fit the 256 MB of the memory-side cache pass it by, others
+    // stay there for their reader: 4096 tokens top-8 of 7168 bf16 (470 MB) 92
+    // against 121 us, but 2048 (235 MB) 48 against 41, 1024 24 against 22.5.
+    const int64_t moved = (int64_t)a.rows * a.H * (f32 ? 4 : 2) * ((a.out ? 1 : 0) + (a.dw ? 1 : 0));
+    const uint32_t threads = 64 * nw;
+    auto run = [&](auto nt) {
+        constexpr bool NT = decltype(nt)::value;
+        if (f32) {
+            if (a.dw)
+                tk_rows_kernel<float, true, NT><<<g, threads, 0, s>>>(a, span);
+            else
+                tk_rows_kernel<float, false, NT><<<g, threads, 0, s>>>(a, span);
+        } else {
+            if (a.dw)
+                tk_rows_kernel<uint16_t, true, NT><<<g, threads, 0, s>>>(a, span);
+            else
+                tk_rows_kernel<uint16_t, false, NT><<<g, threads, 0, s>>>(a, span);
+        }
+    };
+    if (moved > ((int64_t)1 << 28))
+        run(std::true_type{});
+    else
+        run(std::false_type{});
     return hipGetLastError();
 }
 
 hipError_t launch_rows_to_tokens(const TokenArgs& a, bool f32, hipStream_t s) {
     const int chunks = tk_chunks(a, f32);
     const int span = tk_span(a, chunks);
-    const int waves = (span + 63) / 64;
-    const uint32_t nt = 64 * (waves < 4 ? waves : 4);
+    // as many waves as leave the last turn full: 14 waves of columns go in 2 turns of 7
+    const int waves = (span + 63) / 64, turns = (waves + 7) / 8;
+    const uint32_t nt = 64 * ((waves + turns - 1) / turns);
     const dim3 g((uint32_t)a.T, (uint32_t)((chunks + span - 1) / span));
     if (f32) {
         if (a.dw)
