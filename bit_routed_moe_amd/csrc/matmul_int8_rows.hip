@@ -2,10 +2,12 @@
 // into registers, and the time is that of reading them.
 //
 // A workgroup takes one chunk of at most 16 rows of a group and 16 * RT weight
-// rows (SwiGLU: 16 gate rows and the 16 up rows they pair with); its 8 waves
-// share the contraction KW ways (and weight rows 8 / KW ways where the
-// contraction is short).  A step is 256 contraction columns, 4 loads of 64
-// contiguous bytes of each of 16 weight rows, two steps in flight per wave.
+// rows (SwiGLU: 16 gate rows and the 16 up rows they pair with); its 8 waves share the
+// contraction KW ways (and weight rows 8 / KW ways where the contraction is
+// short).  A step is 128 contraction columns, 2 loads of 64 contiguous bytes
+// of each of 16 weight rows, four steps in flight per wave (steps of 256
+// columns, two in flight: 12.1 against 11.3 us at one row of 7168 -> 7168, 4.2
+// against 3.6 at 1024 -> 1024).
 // Weights go first into the matrix instruction (v_mfma_i32_16x16x64_i8), so a
 // lane's results belong to one row.  The waves' sums are joined in LDS.
 //
@@ -20,7 +22,7 @@ namespace ds4 {
 namespace {
 
 constexpr int W8_WAVES = 8;
-constexpr int W8_STEP = 256;   // contraction columns per step
+constexpr int W8_STEP = 128;   // contraction columns per step
 constexpr int W8_REREAD = 20 << 20;   // bytes of weights that all chunks together may read (m8_rows_takes)
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
@@ -112,41 +114,42 @@ __global__ __launch_bounds__(64 * W8_WAVES) void w8_kernel(M8Args a, int kw, int
     i32x4 acc[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) acc[t] = i32x4{0, 0, 0, 0};
-    i32x4 wv[2][RT][4], xv[2][4];
+    i32x4 wv[4][RT][2], xv[4][2];
     auto load = [&](int b, int s) {
         const int c = s * W8_STEP + 16 * q;
 #pragma unroll
         for (int t = 0; t < RT; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) wv[b][t][j] = reinterpret_cast<const i32x4*>(wr[t] + c)[4 * j];
+            for (int j = 0; j < 2; ++j) wv[b][t][j] = reinterpret_cast<const i32x4*>(wr[t] + c)[4 * j];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
             xv[b][j] = i32x4{0, 0, 0, 0};
             if (has) xv[b][j] = reinterpret_cast<const i32x4*>(xr + c)[4 * j];
         }
     };
     auto mma = [&](int b) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int t = 0; t < RT; ++t)
                 acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[b][t][j], xv[b][j], acc[t], 0, 0, 0);
     };
     if (rb * 16 * (GLU ? 1 : RT) < cols) {
-        if (s0 < s1) load(0, s0);
-        if (s0 + 1 < s1) load(1, s0 + 1);
-        for (int s = s0; s < s1; s += 2) {
-            mma(0);
-            if (s + 2 < s1) load(0, s + 2);
-            if (s + 1 < s1) {
-                mma(1);
-                if (s + 3 < s1) load(1, s + 3);
-            }
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            if (s0 + d < s1) load(d, s0 + d);
+        for (int s = s0; s < s1; s += 4) {
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                if (s + d < s1) {
+                    mma(d);
+                    if (s + d + 4 < s1) load(d, s + d + 4);
+                }
         }
         if (kpart == kw - 1 && a.K % W8_STEP) {   // the last columns, masked
             const int c = full * (W8_STEP / 16) + q;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 const i32x4 xt = has ? w8_masked(xr, c + 4 * j, a.K) : i32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
@@ -203,8 +206,10 @@ hipError_t w8_run(const M8Args& a, hipStream_t s) {
     const int most = a.P / 16 + (a.E < a.P ? a.E : a.P), scan = most < a.P;
     const uint32_t gy = !a.offsets ? (uint32_t)((a.P + 15) / 16) : (uint32_t)(scan ? most : a.P);
     const bool glu = a.act == MM_SWIGLU;
-    // two row tiles per wave once there are 4 workgroups per CU with them
-    const bool two = glu || (int64_t)((a.N + 31) / 32) * (a.offsets ? gy : 1) >= 1024 * ng;
+    // two row tiles per wave once that leaves nearly a workgroup per CU: x is read
+    // half as often (16 rows of 7168 -> 7168 13.4 against 16.2 us, one row 11.3
+    // against 11.9)
+    const bool two = glu || (int64_t)((a.N + 31) / 32) * (a.offsets ? gy : 1) >= 200 * ng;
     const int per = glu ? 16 : (two ? 32 : 16), cols = glu ? a.N / 2 : a.N;
     const dim3 g((uint32_t)((cols + per * ng - 1) / (per * ng)), gy);
     if (glu)
