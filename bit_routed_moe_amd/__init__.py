@@ -370,6 +370,7 @@ def _matrix(name, t, dtype, rows, cols, ld, dev):
     shape, strides = t.shape, t.stride()
     # (two dimensions, the ordinary case, first: this is host time of every call)
     if not ((len(shape) == 2 and strides[0] == ld and strides[1] == 1 and shape[0] >= rows and shape[1] >= cols)
+            or (shape and shape[-1] == ld >= cols and t.is_contiguous() and t.numel() >= rows * ld)
             or _rows_apart(shape, strides, rows, cols, ld)):
         raise Ds4MoeError(-2, f"{name} of shape {tuple(shape)}, strides {strides}: not {rows} rows of {cols} "
                               f"elements, {ld} apart")
@@ -474,11 +475,12 @@ def _own_rows(name, t, dtype, rows, cols, q, dev):
     rows of `cols` elements.  (A single row has no stride to be off: the least
     multiple of q.)"""
     shape, strides = t.shape, t.stride()
-    if len(shape) == 2 and rows > 1 and shape[0] >= rows and shape[1] >= cols and strides[1] == 1 and t.dtype is dtype:
+    ld = -(-cols // q) * q if rows == 1 else strides[-2] if len(shape) > 1 and shape[-2] > 1 else cols
+    # (two dimensions first, as in _matrix)
+    if len(shape) == 2 and shape[0] >= rows and shape[1] >= cols and strides[1] == 1 and t.dtype is dtype:
         if t.get_device() != dev:
             raise Ds4MoeError(-1, f"{name} on {t.device}, not on the current HIP device {dev}")
-        return t.data_ptr(), strides[0]
-    ld = -(-cols // q) * q if rows == 1 else strides[-2] if len(shape) > 1 and shape[-2] > 1 else cols
+        return t.data_ptr(), ld
     return _matrix(name, t, dtype, rows, cols, ld, dev), ld
 
 
