@@ -9,6 +9,8 @@
 // that take them.  The column operand goes first into the matrix instruction,
 // so a lane holds 4 consecutive columns of one row; results leave through LDS
 // in whole rows.
+#include <type_traits>
+
 #include "matmul_int8.hpp"
 #include "tile.hpp"
 
@@ -30,7 +32,7 @@ struct M8Operand {
     // tile row and chunk that DMA i of wave w brings for this lane
     static __device__ __forceinline__ int row(int i, int w, int lane) { return (i * NW + w) * RPD + lane / CPR; }
     // what a row's chunks are moved by
-    static __device__ __forceinline__ int place(int row) { return KB == 128 ? (row >> 1) & 7 : (row >> 2) & 3; }
+    static __device__ __forceinline__ int place(int row) { return KB == 128 ? (row >> 1) & 7 : -(row >> 2) & 3; }
     static __device__ __forceinline__ int chunk(int row, int lane) { return (lane % CPR) ^ place(row); }
     // Fragment t (16 tile rows from t0 + 16 * t on) of k-step ks.
     static __device__ __forceinline__ i32x4 frag(const uint8_t* buf, int t0, int t, int ks, int lane) {
@@ -149,7 +151,11 @@ __global__ __launch_bounds__(64 * WR * WC, WPS) void m8_kernel(M8Args a, int tr,
     for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int j = 0; j < MI; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    const int wr0 = (w % WR) * (BR / WR), wc0 = (w / WR) * (BC / WC);
+    // a wave's first row and column of the tile; its row tiles of 16 follow one
+    // another with PIPE, else they alternate with the other waves' (who then
+    // share the rows of a chunk that does not fill the tile)
+    constexpr int RT = PIPE ? 1 : WR;
+    const int wr0 = (w % WR) * (PIPE ? BR / WR : 16), wc0 = (w / WR) * (BC / WC);
     // stages [sb, ns) of the contraction: all, or this split's share
     const int nall = (a.K + KB - 1) / KB;
     const int each = (nall + a.ksplits - 1) / a.ksplits;
@@ -171,7 +177,7 @@ __global__ __launch_bounds__(64 * WR * WC, WPS) void m8_kernel(M8Args a, int tr,
 #pragma unroll
             for (int i = 0; i < NI; ++i)
                 if (i * MI / NI == j) cn[i] = ColOp::frag(buf + RowOp::BYTES, wc0, i, ks, lane);
-            rn[j] = RowOp::frag(buf, wr0, j, ks, lane);
+            rn[j] = RowOp::frag(buf, wr0, RT * j, ks, lane);
 #pragma unroll
             for (int i = 0; i < NI; ++i)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cf[i], rf[j], acc[i][j], 0, 0, 0);
@@ -198,7 +204,7 @@ __global__ __launch_bounds__(64 * WR * WC, WPS) void m8_kernel(M8Args a, int tr,
 #pragma unroll
             for (int i = 0; i < NI; ++i) cf[0][i] = ColOp::frag(lds + (sb % ST) * STB + RowOp::BYTES, wc0, i, 0, lane);
 #pragma unroll
-            for (int j = 0; j < MI; ++j) rf[0][j] = RowOp::frag(lds + (sb % ST) * STB, wr0, j, 0, lane);
+            for (int j = 0; j < MI; ++j) rf[0][j] = RowOp::frag(lds + (sb % ST) * STB, wr0, RT * j, 0, lane);
             for (int st = sb; st < ns; ++st) {
                 step(rf[0], cf[0], rf[1], cf[1], st, 1, -1);
                 // stage st is read; stage st + 1 has to have landed
@@ -218,29 +224,43 @@ __global__ __launch_bounds__(64 * WR * WC, WPS) void m8_kernel(M8Args a, int tr,
             for (int s = 0; s < ST - 1; ++s)
                 if (sb + s < ns) issue(sb + s);
         }
-        for (int st = sb; st < ns; ++st) {
-            if (ST > 2 && st + ST - 2 < ns)
-                mt_wait_vm<(ST - 2) * LPS>();
-            else
-                mt_wait_vm<0>();
-            mt_barrier();
-            if (st + ST - 1 < ns) issue(st + ST - 1);
-            clear_tail(st);
-            const uint8_t* buf = lds + (st % ST) * STB;
+        // Of a chunk with fewer rows than the tile (the end of a group) only
+        // the row tiles that exist are multiplied.
+        auto stages = [&](auto whole) {
+            for (int st = sb; st < ns; ++st) {
+                if (ST > 2 && st + ST - 2 < ns)
+                    mt_wait_vm<(ST - 2) * LPS>();
+                else
+                    mt_wait_vm<0>();
+                mt_barrier();
+                if (st + ST - 1 < ns) issue(st + ST - 1);
+                clear_tail(st);
+                const uint8_t* buf = lds + (st % ST) * STB;
 #pragma unroll
-            for (int ks = 0; ks < KB / 64; ++ks) {
-                i32x4 rf[MI], cf[NI];
+                for (int ks = 0; ks < KB / 64; ++ks) {
+                    i32x4 rf[MI], cf[NI];
 #pragma unroll
-                for (int i = 0; i < NI; ++i) cf[i] = ColOp::frag(buf + RowOp::BYTES, wc0, i, ks, lane);
+                    for (int i = 0; i < NI; ++i) cf[i] = ColOp::frag(buf + RowOp::BYTES, wc0, i, ks, lane);
+                    if constexpr (decltype(whole)::value) {
 #pragma unroll
-                for (int j = 0; j < MI; ++j) rf[j] = RowOp::frag(buf, wr0, j, ks, lane);
+                        for (int j = 0; j < MI; ++j) rf[j] = RowOp::frag(buf, wr0, RT * j, ks, lane);
+                    }
 #pragma unroll
-                for (int j = 0; j < MI; ++j)
+                    for (int j = 0; j < MI; ++j) {
+                        if (decltype(whole)::value || wr0 + 16 * RT * j < ch.n) {
+                            if constexpr (!decltype(whole)::value) rf[j] = RowOp::frag(buf, wr0, RT * j, ks, lane);
 #pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cf[i], rf[j], acc[i][j], 0, 0, 0);
+                            for (int i = 0; i < NI; ++i)
+                                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cf[i], rf[j], acc[i][j], 0, 0, 0);
+                        }
+                    }
+                }
             }
-        }
+        };
+        if (ch.n > BR - 16)
+            stages(std::true_type{});
+        else
+            stages(std::false_type{});
     }
 
     // Out through LDS, RP rows of the wave's tile at a time.  In the
@@ -252,6 +272,7 @@ __global__ __launch_bounds__(64 * WR * WC, WPS) void m8_kernel(M8Args a, int tr,
     static_assert(RP >= 16 && RP % 16 == 0 && RP <= FIT && (CW & (CW - 1)) == 0 && CW >= 32, "passes of whole row tiles");
     int32_t* const part = a.ksplits > 1 ? a.ipart + (size_t)blockIdx.z * a.kpart_stride : nullptr;
     uint8_t* reg = lds + w * (RP * CW * 4);
+    auto row_of = [&](int i) { return wr0 + 16 * RT * (i >> 4) + (i & 15); };   // tile row of the wave's row i
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < WROWS / RP; ++p) {
@@ -262,7 +283,6 @@ __global__ __launch_bounds__(64 * WR * WC, WPS) void m8_kernel(M8Args a, int tr,
             for (int i = 0; i < NI; ++i)
                 *reinterpret_cast<i32x4*>(reg + (16 * j + m) * (CW * 4) + (((4 * i + q) ^ (m & (CW / 4 - 1))) << 4)) =
                     acc[i][p * (RP / 16) + j];
-        const int rbase = wr0 + p * RP;
         if (glu) {
             // 16 gate columns, then the 16 up columns they pair with
             constexpr int LR = CW / 16;   // lanes per row
@@ -274,8 +294,9 @@ __global__ __launch_bounds__(64 * WR * WC, WPS) void m8_kernel(M8Args a, int tr,
                 int32_t g[8], u[8];
                 m8_get8<CW>(reg, rr, col, g);
                 m8_get8<CW>(reg, rr, col + 16, u);
-                if (rbase + rr >= ch.n || cnt <= 0) continue;
-                const int r = ch.row0 + rbase + rr;
+                const int at = row_of(p * RP + rr);
+                if (at >= ch.n || cnt <= 0) continue;
+                const int r = ch.row0 + at;
                 if (part) {
                     int32_t* o = part + (size_t)r * a.ldp + f;
                     m8_part8(o, g, cnt, cnt >= 8);
@@ -295,8 +316,9 @@ __global__ __launch_bounds__(64 * WR * WC, WPS) void m8_kernel(M8Args a, int tr,
             for (int rr = lane / LR; rr < RP; rr += 64 / LR) {
                 int32_t v[8];
                 m8_get8<CW>(reg, rr, col, v);
-                if (rbase + rr >= ch.n || cnt <= 0) continue;
-                const int r = ch.row0 + rbase + rr;
+                const int at = row_of(p * RP + rr);
+                if (at >= ch.n || cnt <= 0) continue;
+                const int r = ch.row0 + at;
                 if (part) {
                     m8_part8(part + (size_t)r * a.ldp + n, v, cnt, cnt >= 8);
                 } else {
