@@ -603,9 +603,11 @@ int m8_call(const ds4moe_matmul_int8* m, int32_t rows, ds4::M8Args& a, const int
         int32_t* n = reinterpret_cast<int32_t*>(ws + L.plan);
         ds4::MmChunk* c = reinterpret_cast<ds4::MmChunk*>(ws + L.plan + 256);
         a.max_chunks = mm_max_chunks(&mm, rows, bm);
-        TRY(hip_status(ds4::launch_mm_plan(a, bm, c, n, s), "matmul int8: plan"));
-        a.chunks = c;
-        a.n_chunks = n;
+        if (ds4::m8_wants_plan(a.P, a.K, a.N, a.E)) {
+            TRY(hip_status(ds4::launch_mm_plan(a, bm, c, n, s), "matmul int8: plan"));
+            a.chunks = c;
+            a.n_chunks = n;
+        }
     }
     return hip_status(ds4::launch_m8(a, m->dtype == DS4MOE_DT_F32, s), "matmul int8");
 }

@@ -94,25 +94,63 @@ __global__ __launch_bounds__(64 * WR * WC, WPS) void m8_kernel(M8Args a, int tr,
 
     // this workgroup's tile: each of the 8 XCDs (workgroup id modulo 8) takes
     // a contiguous eighth of the tiles that exist
-    const int ntr = a.chunks ? a.n_chunks[0] : tr;
-    const int total = ntr * tc, per = (total + 7) >> 3, slot = (int)blockIdx.x >> 3;
-    const int t = ((int)blockIdx.x & 7) * per + slot;
-    if (slot >= per || t >= total) return;
-    int rt, ct;
-    if (a.chunks) {   // a group's tiles follow one another, so that its weights are read once
+    const int slot = (int)blockIdx.x >> 3;
+    auto tile_of = [&](int ntr, int& t) {
+        const int total = ntr * tc, per = (total + 7) >> 3;
+        t = ((int)blockIdx.x & 7) * per + slot;
+        return slot < per && t < total;
+    };
+    int t, rt, ct;
+    MmChunk ch;
+    if (a.E > 1 && !a.chunks) {
+        // without a plan: a scan over the groups' numbers of chunks (a group's
+        // tiles follow one another, so that its weights are read once)
+        __shared__ int tmp[32], found[4];
+        constexpr int G = 1024 / (64 * NW);
+        int r0[G], cnt[G], sum = 0, total;
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            r0[i] = cnt[i] = 0;
+            if (G * tid + i < a.E) mm_group_rows(a.offsets, G * tid + i, a.P, r0[i], cnt[i]);
+            sum += (cnt[i] + BR - 1) / BR;
+        }
+        int first = block_exclusive_scan(sum, tmp, &total);
+        if (!tile_of(min(total, a.max_chunks), t)) return;
         const int c = t / tc;
-        const MmChunk o = a.chunks[c];
-        int r0, n;
-        mm_group_rows(a.offsets, o.group, a.P, r0, n);
-        const int first = c - o.index;
-        mt_tile(t - first * tc, (n + BR - 1) / BR, tc, rt, ct);
-        rt += first;
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const int n = (cnt[i] + BR - 1) / BR;
+            if (c >= first && c < first + n) {
+                found[0] = G * tid + i;
+                found[1] = r0[i];
+                found[2] = cnt[i];
+                found[3] = first;
+            }
+            first += n;
+        }
+        __syncthreads();
+        const int n = __builtin_amdgcn_readfirstlane(found[2]);
+        mt_tile(t - __builtin_amdgcn_readfirstlane(found[3]) * tc, (n + BR - 1) / BR, tc, rt, ct);
+        ch.group = __builtin_amdgcn_readfirstlane(found[0]);
+        ch.row0 = __builtin_amdgcn_readfirstlane(found[1]) + rt * BR;
+        ch.n = min(BR, n - rt * BR);
     } else {
-        mt_tile(t, ntr, tc, rt, ct);
+        const int ntr = a.chunks ? a.n_chunks[0] : tr;
+        if (!tile_of(ntr, t)) return;
+        if (a.chunks) {
+            const int c = t / tc;
+            const MmChunk o = a.chunks[c];
+            int r0, n;
+            mm_group_rows(a.offsets, o.group, a.P, r0, n);
+            const int first = c - o.index;
+            mt_tile(t - first * tc, (n + BR - 1) / BR, tc, rt, ct);
+            rt += first;
+        } else {
+            mt_tile(t, ntr, tc, rt, ct);
+        }
+        if (!mm_chunk(a, rt, BR, ch)) return;
     }
     const int c0 = ct * BC;
-    MmChunk ch;
-    if (!mm_chunk(a, rt, BR, ch)) return;
     const bool glu = a.act == MM_SWIGLU;
     const int8_t* const wg = static_cast<const int8_t*>(a.w) + (size_t)ch.group * a.N * a.ldw;
 
@@ -400,6 +438,7 @@ constexpr M8Shape M8_SHAPES[] = {
 constexpr int M8_NSHAPES = 5;
 constexpr double M8_ENDS = 2.35;   // us to fill a workgroup's first stages and to write its tile
 constexpr double M8_JOIN = 3.0;    // us of a join launch
+constexpr double M8_SCANS = 2.0;   // rounds of workgroups up to which each scans for its chunk
 constexpr double M8_MEM = 4.2e6;   // bytes per us, of outputs and partial sums
 
 struct M8Pick {
@@ -439,7 +478,7 @@ M8Pick m8_pick(int P, int K, int N, int E) {
 
 template <int BR, int BC, int WR, int WC, int KB, int ST, bool PIPE, int WPS, typename T>
 hipError_t m8_launch(const M8Args& a, hipStream_t s) {
-    const int tr = a.chunks ? a.max_chunks : cdiv(a.P, BR), tc = cdiv(a.N, BC);
+    const int tr = a.E > 1 ? a.max_chunks : cdiv(a.P, BR), tc = cdiv(a.N, BC);
     const int64_t total = (int64_t)tr * tc;
     const dim3 g((uint32_t)((total + 7) / 8 * 8), 1, (uint32_t)a.ksplits);
     m8_kernel<BR, BC, WR, WC, KB, ST, PIPE, WPS, T><<<g, 64 * WR * WC, 0, s>>>(a, tr, tc);
@@ -464,7 +503,14 @@ hipError_t m8_run(const M8Args& a, int shape, hipStream_t s) {
 }  // namespace
 
 int m8_chunk_rows(int P, int K, int N, int E) {
-    return m8_rows_takes(P, K, N, E) ? 0 : M8_SHAPES[m8_pick(P, K, N, E).shape].br;
+    return E == 1 || m8_rows_takes(P, K, N, E) ? 0 : M8_SHAPES[m8_pick(P, K, N, E).shape].br;
+}
+
+bool m8_wants_plan(int P, int K, int N, int E) {
+    const M8Pick pick = m8_pick(P, K, N, E);
+    const M8Shape& t = M8_SHAPES[pick.shape];
+    const double tiles = ((double)P / t.br + 0.5 * (E < P ? E : P)) * cdiv(N, t.bc);
+    return pick.splits > 1 || tiles > M8_SCANS * 256.0 * t.wgs;
 }
 
 size_t m8_split_bytes(int P, int K, int N, int E, bool exact) {

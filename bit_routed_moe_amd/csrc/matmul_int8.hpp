@@ -95,8 +95,10 @@ __device__ __forceinline__ void m8_out8(const M8Args& a, int r, int n, int cnt, 
     m8_st8(static_cast<T*>(a.y) + o, z, cnt, cnt >= 8);
 }
 
-// Rows per chunk of a grouped call's plan (0: no plan).
+// Rows per chunk of a grouped call on the tile kernels (0: not one of those),
+// and whether its chunks are listed by a plan launch (else each workgroup scans).
 int m8_chunk_rows(int P, int K, int N, int E);
+bool m8_wants_plan(int P, int K, int N, int E);
 // Scratch of a launch (M8Args::ipart): for these rows, or a bound for all up to P.
 size_t m8_split_bytes(int P, int K, int N, int E, bool exact);
 hipError_t launch_m8(const M8Args& a, bool f32, hipStream_t s);
