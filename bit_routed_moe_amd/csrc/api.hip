@@ -554,12 +554,14 @@ struct M8Layout {
     size_t plan, split, total;
 };
 
-M8Layout m8_layout(const ds4moe_matmul_int8* m, int32_t rows, bool call) {
+// pick: what this call takes; null: a bound for all calls of up to `rows` rows.
+M8Layout m8_layout(const ds4moe_matmul_int8* m, int32_t rows, const ds4::M8Pick* pick) {
     M8Layout L{};
     const ds4moe_matmul mm = m8_as_mm(m);
     if (m->groups > 1)
         L.split = align256(256 + sizeof(ds4::MmChunk) * (size_t)mm_max_chunks(&mm, rows, ds4::MM_MIN_CHUNK));
-    L.total = align256(L.split + ds4::m8_split_bytes(rows, m->in_dim, m->out_dim, m->groups, call));
+    L.total = align256(L.split + (pick ? ds4::m8_split_bytes(*pick, rows, m->out_dim)
+                                       : ds4::m8_split_bound(rows, m->in_dim, m->out_dim)));
     return L;
 }
 
@@ -593,23 +595,24 @@ int m8_call(const ds4moe_matmul_int8* m, int32_t rows, ds4::M8Args& a, const int
     a.bias = bias;
     a.residual = residual;
     a.y = y;
-    const M8Layout L = m8_layout(m, rows, true);
+    const ds4::M8Pick pick = ds4::m8_pick(a.P, a.K, a.N, a.E);
+    const M8Layout L = m8_layout(m, rows, &pick);
     TRY(check_workspace(workspace, workspace_bytes, L.total));
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.ipart = reinterpret_cast<int32_t*>(ws + L.split);
-    const int bm = m->groups > 1 ? ds4::m8_chunk_rows(a.P, a.K, a.N, a.E) : 0;
+    const int bm = m->groups > 1 ? ds4::m8_chunk_rows(pick) : 0;
     if (bm) {
         const ds4moe_matmul mm = m8_as_mm(m);
         int32_t* n = reinterpret_cast<int32_t*>(ws + L.plan);
         ds4::MmChunk* c = reinterpret_cast<ds4::MmChunk*>(ws + L.plan + 256);
         a.max_chunks = mm_max_chunks(&mm, rows, bm);
-        if (ds4::m8_wants_plan(a.P, a.K, a.N, a.E)) {
+        if (ds4::m8_wants_plan(pick, a.P, a.N, a.E)) {
             TRY(hip_status(ds4::launch_mm_plan(a, bm, c, n, s), "matmul int8: plan"));
             a.chunks = c;
             a.n_chunks = n;
         }
     }
-    return hip_status(ds4::launch_m8(a, m->dtype == DS4MOE_DT_F32, s), "matmul int8");
+    return hip_status(ds4::launch_m8(a, pick, m->dtype == DS4MOE_DT_F32, s), "matmul int8");
 }
 
 }  // namespace
@@ -1179,7 +1182,7 @@ int ds4moe_quantize_rows_int8(int32_t rows, int32_t cols, int32_t dtype, const v
 
 size_t ds4moe_matmul_int8_workspace_bytes(const ds4moe_matmul_int8* m, int32_t rows) {
     if (check_m8(m, rows) != DS4MOE_OK) return 0;
-    return m8_layout(m, rows, false).total;
+    return m8_layout(m, rows, nullptr).total;
 }
 
 int ds4moe_linear_int8(const ds4moe_matmul_int8* m, int32_t rows, const int8_t* xq, const float* x_scale,

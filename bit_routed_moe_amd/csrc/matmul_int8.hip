@@ -438,20 +438,18 @@ constexpr M8Shape M8_SHAPES[] = {
 constexpr int M8_NSHAPES = 5;
 constexpr double M8_ENDS = 2.35;   // us to fill a workgroup's first stages and to write its tile
 constexpr double M8_JOIN = 3.0;    // us of a join launch
-constexpr double M8_SCANS = 2.0;   // rounds of workgroups up to which each scans for its chunk
+// Rounds of workgroups up to which each scans for its chunk: 256 rows of 8 groups
+// 2048 -> 2048 13.2 us against 14.9 with a plan launch, 4096 of 8 41.8 / 42.3,
+// but 32768 of 64 256 -> 4096 290 / 249, 16000 of 1000 512 -> 512 78 / 63.
+constexpr double M8_SCANS = 2.0;
 constexpr double M8_MEM = 4.2e6;   // bytes per us, of outputs and partial sums
-
-struct M8Pick {
-    int shape, splits;
-};
 
 // Tile shape and contraction splits of the least estimated time: a CU's
 // workgroups times their stages, plus what does not overlap.
-M8Pick m8_pick(int P, int K, int N, int E) {
+M8Pick m8_tile_pick(int P, int K, int N, int E) {
     const int live = E < P ? E : P;
     const int ns = cdiv(K, M8_K);
-    M8Pick best{0, 1};
-    double least = 1e300;
+    M8Pick best{0, 1, 1e300};
     for (int i = 0; i < M8_NSHAPES; ++i) {
         const M8Shape& t = M8_SHAPES[i];
         double tr = cdiv(P, t.br);   // row tiles; of ragged groups about half a tile each is not filled
@@ -467,10 +465,7 @@ M8Pick m8_pick(int P, int K, int N, int E) {
             else
                 us = (us > out ? us : out) + M8_ENDS;
             if (s > 1) us += M8_JOIN + (double)wgs * t.br * t.bc * 8.0 / M8_MEM;
-            if (us < least) {
-                least = us;
-                best = M8Pick{i, s};
-            }
+            if (us < best.us) best = M8Pick{i, s, us};
         }
     }
     return best;
@@ -502,34 +497,34 @@ hipError_t m8_run(const M8Args& a, int shape, hipStream_t s) {
 
 }  // namespace
 
-int m8_chunk_rows(int P, int K, int N, int E) {
-    return E == 1 || m8_rows_takes(P, K, N, E) ? 0 : M8_SHAPES[m8_pick(P, K, N, E).shape].br;
+M8Pick m8_pick(int P, int K, int N, int E) {
+    const M8Pick tile = m8_tile_pick(P, K, N, E);
+    return m8_rows_takes(P, K, N, E, tile.us) ? M8Pick{-1, 1, 0.0} : tile;
 }
 
-bool m8_wants_plan(int P, int K, int N, int E) {
-    const M8Pick pick = m8_pick(P, K, N, E);
+int m8_chunk_rows(const M8Pick& pick) { return pick.shape < 0 ? 0 : M8_SHAPES[pick.shape].br; }
+
+bool m8_wants_plan(const M8Pick& pick, int P, int N, int E) {
     const M8Shape& t = M8_SHAPES[pick.shape];
     const double tiles = ((double)P / t.br + 0.5 * (E < P ? E : P)) * cdiv(N, t.bc);
     return pick.splits > 1 || tiles > M8_SCANS * 256.0 * t.wgs;
 }
 
-size_t m8_split_bytes(int P, int K, int N, int E, bool exact) {
-    // the bound: at most 512 tiles of up to 128 x 128 in all splits together,
-    // and at most M8_MAX_SPLITS splits
+size_t m8_split_bytes(const M8Pick& pick, int P, int N) {
+    return pick.splits > 1 ? (size_t)pick.splits * P * ((N + 7) / 8 * 8) * 4 : 0;
+}
+
+size_t m8_split_bound(int P, int K, int N) {
+    // at most 512 tiles of up to 128 x 128 in all splits together, and at most
+    // M8_MAX_SPLITS splits
     if (cdiv(K, M8_K) < 8) return 0;
-    const int64_t one = (int64_t)P * ((N + 7) / 8 * 8);
-    if (exact) {
-        const int splits = m8_rows_takes(P, K, N, E) ? 1 : m8_pick(P, K, N, E).splits;
-        return splits > 1 ? (size_t)splits * one * 4 : 0;
-    }
-    const int64_t all = M8_MAX_SPLITS * one, cap = (int64_t)512 * 128 * 128;
+    const int64_t all = M8_MAX_SPLITS * (int64_t)P * ((N + 7) / 8 * 8), cap = (int64_t)512 * 128 * 128;
     return (size_t)(all < cap ? all : cap) * 4;
 }
 
-hipError_t launch_m8(const M8Args& a0, bool f32, hipStream_t s) {
-    if (m8_rows_takes(a0.P, a0.K, a0.N, a0.E)) return launch_m8_rows(a0, f32, s);
+hipError_t launch_m8(const M8Args& a0, const M8Pick& pick, bool f32, hipStream_t s) {
+    if (pick.shape < 0) return launch_m8_rows(a0, f32, s);
     M8Args a = a0;
-    const M8Pick pick = m8_pick(a.P, a.K, a.N, a.E);
     a.ksplits = pick.splits;
     a.ldp = (a.N + 7) / 8 * 8;
     a.kpart_stride = (size_t)a.P * a.ldp;

@@ -95,16 +95,25 @@ __device__ __forceinline__ void m8_out8(const M8Args& a, int r, int n, int cnt, 
     m8_st8(static_cast<T*>(a.y) + o, z, cnt, cnt >= 8);
 }
 
-// Rows per chunk of a grouped call on the tile kernels (0: not one of those),
-// and whether its chunks are listed by a plan launch (else each workgroup scans).
-int m8_chunk_rows(int P, int K, int N, int E);
-bool m8_wants_plan(int P, int K, int N, int E);
-// Scratch of a launch (M8Args::ipart): for these rows, or a bound for all up to P.
-size_t m8_split_bytes(int P, int K, int N, int E, bool exact);
-hipError_t launch_m8(const M8Args& a, bool f32, hipStream_t s);
+// What a product runs on: a tile shape and its splits of the contraction, or
+// the few-row kernel (shape < 0).
+struct M8Pick {
+    int shape, splits;
+    double us;   // estimated
+};
+M8Pick m8_pick(int P, int K, int N, int E);
+// Rows per chunk of a grouped call (0 on the few-row kernel), and whether its
+// chunks are listed by a plan launch (else each workgroup scans).
+int m8_chunk_rows(const M8Pick& pick);
+bool m8_wants_plan(const M8Pick& pick, int P, int N, int E);
+// Scratch of a launch (M8Args::ipart), and a bound for all up to P rows.
+size_t m8_split_bytes(const M8Pick& pick, int P, int N);
+size_t m8_split_bound(int P, int K, int N);
+hipError_t launch_m8(const M8Args& a, const M8Pick& pick, bool f32, hipStream_t s);
 
-// Products of few rows (matmul_int8_rows.hip).
-bool m8_rows_takes(int P, int K, int N, int E);
+// Products of few rows (matmul_int8_rows.hip): whether they run there, given
+// the best tile shape's estimate.
+bool m8_rows_takes(int P, int K, int N, int E, double tile_us);
 hipError_t launch_m8_rows(const M8Args& a, bool f32, hipStream_t s);
 
 }  // namespace ds4

@@ -23,7 +23,6 @@ namespace {
 
 constexpr int W8_WAVES = 8;
 constexpr int W8_STEP = 128;   // contraction columns per step
-constexpr int W8_REREAD = 20 << 20;   // bytes of weights that all chunks together may read (m8_rows_takes)
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 // 16 bytes of a row from chunk c on; bytes from column K on are zero.
@@ -199,17 +198,26 @@ int w8_kw(int K) {
     return kw;
 }
 
+// Workgroup rows of a grouped call: one per chunk that there can be, or per row
+// where that is fewer.
+int w8_rows_of_grid(int P, int E) {
+    const int most = P / 16 + (E < P ? E : P);
+    return most < P ? most : P;
+}
+
+// Two row tiles per wave once that leaves nearly a workgroup per CU: x is read
+// half as often (16 rows of 7168 -> 7168 13.4 against 16.2 us, one row 11.3
+// against 11.9).
+bool w8_two(int N, int gy, int ng) { return (int64_t)((N + 31) / 32) * gy >= 200 * ng; }
+
 template <typename T>
 hipError_t w8_run(const M8Args& a, hipStream_t s) {
     const int kw = w8_kw(a.K), ng = W8_WAVES / kw;
-    // grouped: a workgroup row per chunk that there can be, or per row where that is fewer
-    const int most = a.P / 16 + (a.E < a.P ? a.E : a.P), scan = most < a.P;
-    const uint32_t gy = !a.offsets ? (uint32_t)((a.P + 15) / 16) : (uint32_t)(scan ? most : a.P);
+    const int most = a.offsets ? w8_rows_of_grid(a.P, a.E) : 1;
+    const int scan = a.offsets && most < a.P;
+    const uint32_t gy = a.offsets ? (uint32_t)most : (uint32_t)((a.P + 15) / 16);
     const bool glu = a.act == MM_SWIGLU;
-    // two row tiles per wave once that leaves nearly a workgroup per CU: x is read
-    // half as often (16 rows of 7168 -> 7168 13.4 against 16.2 us, one row 11.3
-    // against 11.9)
-    const bool two = glu || (int64_t)((a.N + 31) / 32) * (a.offsets ? gy : 1) >= 200 * ng;
+    const bool two = glu || w8_two(a.N, most, ng);
     const int per = glu ? 16 : (two ? 32 : 16), cols = glu ? a.N / 2 : a.N;
     const dim3 g((uint32_t)((cols + per * ng - 1) / (per * ng)), gy);
     if (glu)
@@ -223,22 +231,27 @@ hipError_t w8_run(const M8Args& a, hipStream_t s) {
 
 }  // namespace
 
-// Products that take these kernels.  Every chunk of 16 rows reads the weights
-// again, from L2 when they are small: us here / with the best tile shape,
-//   dense: 301 x 1459 -> 331 4.8 / 8.3, 600 6.4 / 8.4, 1200 10.4 / 8.5; 300 x
-//     7168 -> 100 9.9 / 13.7; 64 x 4096 -> 1024 6.5 / 8.7, 64 x 8192 -> 512 9.8
-//     / 9.3; 32 x 4096 -> 4096 10.2 / 9.5, 64 x 4096 -> 4096 17.6 / 11.0.
-//   grouped (the tiles need a plan launch): 903 rows of 7 experts 459 -> 331 7.4
-//     / 9.3, 637 of 13 1570 -> 244 8.0 / 13.4, 512 of 64 1024 -> 1024 19 / 18,
-//     256 of 8 2048 -> 2048 22 / 13.
-// With the border at 20 MB read by all chunks together none of 65 products
-// timed both ways loses more than 6%.  Up to 16 rows the weights come from
-// memory once in either kernel, and these read them faster.
-bool m8_rows_takes(int P, int K, int N, int E) {
-    const double chunks = P / 16.0 + (E == 1 ? 0.5 : (E < P ? E : P) / 2.0);   // about
-    if (chunks * N * K <= (double)W8_REREAD) return true;
-    if (E > 1) return P <= 16 || (P <= 256 && P <= 2 * E);
-    return P <= 8 || (P <= 16 && N < 32768);
+// Products that take these kernels.  Up to 8 rows (16 below 32768 columns;
+// grouped 16, or 256 at two per group) the weights come from memory once in
+// either kernel, and these read them faster: 9 rows of 7168 -> 7168 13.3 us
+// against 16.0 on the tiles, 16 of 7168 -> 131072 176 / 162, 64 of 256 groups
+// 7168 -> 4096 269 / 300, 256 of 256 807 / 817; at worst 12 rows of 4096 ->
+// 16384 17.0 / 16.0.  More rows read small weights again from L2 for each 16,
+// which the tiles' latency outlasts for a while (301 x 1459 -> 331 4.8 / 8.3,
+// 1200 10.4 / 8.5; 903 rows of 7 groups 459 -> 331 7.0 / 9.3): there an estimate
+// decides, of the time for all workgroups, for a wave's steps and for the bytes
+// read.  Of 175 products timed both ways it is over 8% off in 3, at most 16%.
+bool m8_rows_takes(int P, int K, int N, int E, double tile_us) {
+    if (E > 1 ? P <= 16 || (P <= 256 && P <= 2 * E) : P <= 8 || (P <= 16 && N < 32768)) return true;
+    const int kw = w8_kw(K), ng = W8_WAVES / kw;
+    const double chunks = E == 1 ? (P + 15) / 16 : P / 16.0 + (E < P ? E : P) / 2.0;
+    const bool two = w8_two(N, E == 1 ? 1 : w8_rows_of_grid(P, E), ng);
+    const int per = (two ? 32 : 16) * ng;
+    const double wgs = chunks * ((N + per - 1) / per) / 256.0;   // per CU
+    const int steps = ((K / W8_STEP + kw - 1) / kw + (K % W8_STEP != 0)) * (two ? 2 : 1);
+    const double mb = chunks * N * K / (1 << 20);
+    if (E == 1) return 3.53 + 1.12 * wgs + 0.226 * steps + 0.06 * mb < tile_us + 2.75;
+    return 4.3 + 1.51 * wgs + 0.024 * steps + 0.161 * mb < tile_us + 4.25;   // (a plan, or scans, on top)
 }
 
 hipError_t launch_m8_rows(const M8Args& a, bool f32, hipStream_t s) {
