@@ -243,6 +243,7 @@ hipError_t w8_run(const M8Args& a, hipStream_t s) {
 // read.  Of 175 products timed both ways it is over 8% off in 3, at most 16%.
 bool m8_rows_takes(int P, int K, int N, int E, double tile_us) {
     if (E > 1 ? P <= 16 || (P <= 256 && P <= 2 * E) : P <= 8 || (P <= 16 && N < 32768)) return true;
+    if (P > 1 << 19) return false;   // (chunks are a dimension of the grid, at most 65535)
     const int kw = w8_kw(K), ng = W8_WAVES / kw;
     const double chunks = E == 1 ? (P + 15) / 16 : P / 16.0 + (E < P ? E : P) / 2.0;
     const bool two = w8_two(N, E == 1 ? 1 : w8_rows_of_grid(P, E), ng);

@@ -390,6 +390,44 @@ def test_graph_replays_and_streams(kw):
         assert torch.equal(a, want) and torch.equal(b, want)
 
 
+@pytest.mark.parametrize("rows,K,N,act", [(1500, 64, 72, "none"), (900, 300, 130, "swiglu"), (9000, 200, 64, "silu"),
+                                          (40, 2000, 33, "none")])
+def test_1024_groups(rows, K, N, act):
+    """The most groups, most of them empty or of one row: by the few-row kernel, by tiles that scan, by a plan."""
+    g = torch.Generator().manual_seed(rows)
+    groups = torch.bincount(torch.randint(0, 1024, (rows,), generator=g), minlength=1024).tolist()
+    for k in (0, 5):
+        p = Problem(rows, K, N, "bf16", act=act, groups=groups, gather_k=k, bias=True, seed=k)
+        p.run()
+        p.check()
+
+
+@pytest.mark.parametrize("groups", [[40], [300], [700, 5], [3, 0, 9]])
+def test_offsets_that_start_behind_zero(groups):
+    """Rows before the first group and behind the last are left as they were."""
+    first, behind = 7, 11
+    n = sum(groups)
+    p = Problem(first + n + behind, 330, 150, "f32", groups=groups, bias=True, seed=n)
+    p.off += first
+    p.off_h = [o + first for o in p.off_h]
+    p.run()
+    p.check()
+
+
+def test_many_rows_of_one_column():
+    """A product whose chunks of 16 rows are more than a grid's second dimension holds."""
+    P, K = (1 << 20) + 5, 48
+    g = torch.Generator().manual_seed(3)
+    x = torch.randint(-128, 128, (P, K), generator=g, dtype=torch.int8).to(DEV)
+    w = torch.randint(-128, 128, (3, K), generator=g, dtype=torch.int8).to(DEV)
+    y = torch.full((P, 4), float("nan"), device=DEV)
+    m = ds4.make_matmul_int8(K, 3, dtype="f32", ldy=4)
+    n = ds4.matmul_int8_workspace_bytes(m, P)
+    ds4.linear_int8(m, P, x, torch.ones(P, device=DEV), w, torch.ones(3, device=DEV), y,
+                    workspace=torch.empty(n, dtype=torch.uint8, device=DEV) if n else None)
+    assert torch.equal(y[:, :3].double(), torch.matmul(x.double(), w.double().t())) and y[:, 3].isnan().all()
+
+
 def test_experts_in_8_bits_to_the_next_token():
     """A layer's way through the calls: route, permute, rows to codes, gate/up products by expert, codes again, down
     products, the rows collected, the head's product, rules on its logits, sampling.  Each stage is checked against

@@ -244,6 +244,32 @@ def test_far_rows():
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("B,V", [(5, 1 << 20), (32768, 9), (2, (1 << 20) - 1), (1025, 4097), (600, 8191)])
+def test_limits(B, V):
+    """The most tokens and rows, and borders of the segments, against torch's own scatter of one rule each."""
+    g = torch.Generator().manual_seed(B)
+    l = torch.empty(B, V).normal_(generator=g).to(DEV)
+    n = torch.randint(0, 4, (B,), generator=g)
+    off = torch.zeros(B + 1, dtype=torch.int32)
+    off[1:] = n.cumsum(0)
+    total = int(off[-1])
+    tok = torch.randint(0, V, (total,), generator=g)
+    row = torch.repeat_interleave(torch.arange(B), n)
+    freq = torch.rand(B, generator=g)
+    mask = torch.randint(-2 ** 31, 2 ** 31, (B, (V + 31) // 32), generator=g, dtype=torch.int64).int()
+    out = torch.full((B, V), float("nan"), device=DEV)
+    ds4.adjust_logits(B, V, l, out, history=tok.int().to(DEV), history_offsets=off.to(DEV), frequency=freq.to(DEV),
+                      mask=mask.to(DEV))
+    count = torch.zeros(B, V, dtype=torch.float64, device=DEV)
+    count.index_put_((row.to(DEV), tok.to(DEV)), torch.ones(total, dtype=torch.float64, device=DEV), accumulate=True)
+    want = l.double() - freq.double().to(DEV)[:, None] * count
+    bit = (mask.to(DEV)[:, :, None] >> torch.arange(32, dtype=torch.int32, device=DEV)) & 1
+    allowed = bit.reshape(B, -1)[:, :V] == 1
+    assert (out[~allowed] == -INF).all()
+    tol = (count > 0) * 4 * 2.0 ** -24 * (l.double().abs() + count)
+    assert ((out.double() - want).abs()[allowed] <= tol[allowed]).all()
+
+
 def test_then_sample():
     """Penalties, a ban and a mask carry through to the choice; a row whose mask leaves nothing has no token."""
     B, V = 6, 70001

@@ -207,6 +207,37 @@ def test_far_rows(which):
         assert ((y.double() - want).abs() <= HALF["bf16"] * want.abs() + 2.0 ** -22 * vals.double().abs().view(T, 2, H).sum(1)).all()
 
 
+@pytest.mark.parametrize("layout", ["sorted", "roomy"])
+def test_rows_that_no_cache_holds(layout):
+    """Rows of more than 256 MB, which are stored another way."""
+    T, k, H = 4100, 8, 4104
+    c = Case(T, k, H, "bf16", layout=layout, seed=21)
+    for zeros in (False, True):
+        sp = c.sorted_pair if zeros else None
+        buf, out, _ = matrix(c.rows, H, "bf16")
+        ds4.dispatch(c.d, T, c.rows, c.tok, c.pos, out, topk_w=c.w, sorted_pair=sp)
+        c.check_rows(buf, out, torch.full_like(out, float("nan")), zeros)
+    rows, dw = c.row_buf.clone(), torch.empty(T, k, device=DEV)
+    ds4.collect_backward(c.d, T, c.rows, c.tok, c.pos, expert_rows=rows[:, :H], topk_w=c.w, sorted_pair=c.sorted_pair,
+                         drows=rows[:, :H], dtopk_w=dw)
+    c.check_rows(rows, rows[:, :H], None, True)
+    c.check_dots(dw)
+
+
+@pytest.mark.parametrize("T,k,H,dtype", [(1 << 20, 1, 8, "bf16"), (2, 2, 1 << 20, "f32"), (3, 1, (1 << 20) - 3, "bf16"),
+                                         (1 << 17, 8, 4, "f32")])
+def test_limits(T, k, H, dtype):
+    c = Case(T, k, H, dtype, layout="roomy", seed=22)
+    buf, out, _ = matrix(c.rows, H, dtype)
+    ds4.dispatch(c.d, T, c.rows, c.tok, c.pos, out, topk_w=c.w, sorted_pair=c.sorted_pair)
+    c.check_rows(buf, out, None, True)
+    buf, dx, _ = matrix(T, H, dtype)
+    dw = torch.full((T, k), float("nan"), device=DEV)
+    ds4.dispatch_backward(c.d, T, c.rows, c.row, c.pos, topk_w=c.w, x=c.tok, dx=dx, dtopk_w=dw)
+    c.check_sums(buf, dx, None)
+    c.check_dots(dw)
+
+
 # ---- the router's gradient -----------------------------------------------------------
 
 @pytest.mark.parametrize("T,E,k", [(1, 8, 2), (5, 256, 8), (1, 1, 1), (67, 1024, 64), (300, 100, 7), (2, 65, 64)])

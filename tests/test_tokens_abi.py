@@ -156,3 +156,28 @@ def test_binding_route_backward(lib):
             with pytest.raises(ds4.Ds4MoeError, match=n) as e:
                 ds4.route_backward(cfg, T, **dict(good, **{n: bad}))
             assert e.value.status == st and not lib.called
+
+
+def test_other_devices_are_refused(monkeypatch):
+    """Tensors on the host (or another device) while device 0 is current."""
+    monkeypatch.setattr(ds4, "lib", Recorder())
+    monkeypatch.setattr(ds4, "_here", lambda: 0)
+    monkeypatch.setattr(ds4, "_s", lambda *args: None)
+    d, cfg = ds4.make_rows(H, K), ds4.make_config(256, 128, 8, K)
+    m = ds4.make_matmul_int8(32, 16, groups=1)
+    row = lambda n, w=H, t=BF: torch.zeros(n, w, dtype=t)
+    i32 = lambda n: torch.zeros(n, dtype=I32)
+    i8 = lambda n: torch.zeros(n, 32, dtype=torch.int8)
+    f = torch.zeros
+    for call in (lambda: ds4.dispatch(d, T, R, row(T), i32(T * K), row(R)),
+                 lambda: ds4.collect(d, T, R, row(R), i32(T * K), row(T)),
+                 lambda: ds4.dispatch_backward(d, T, R, row(R), i32(T * K), dx=row(T)),
+                 lambda: ds4.collect_backward(d, T, R, row(T), i32(T * K), drows=row(R)),
+                 lambda: ds4.route_backward(cfg, T, i32(T * K), f(T * K), f(T * K), f(T * 8)),
+                 lambda: ds4.quantize_rows_int8(4, 32, row(4, 32), i8(4), f(4)),
+                 lambda: ds4.linear_int8(m, 4, i8(4), f(4), i8(16), f(16), row(4, 16)),
+                 lambda: ds4.grouped_matmul_int8(m, 4, i8(4), f(4), i8(16), f(16), i32(2), row(4, 16)),
+                 lambda: ds4.adjust_logits(2, 50, f(2, 50), f(2, 50), bias_token=i32(1), bias_value=f(1), bias_offsets=i32(3))):
+        with pytest.raises(ds4.Ds4MoeError, match="not on the current HIP device") as e:
+            call()
+        assert e.value.status == -1 and not ds4.lib.called
