@@ -1,14 +1,29 @@
 // Products in 8-bit integers on the matrix cores (v_mfma_i32_16x16x64_i8).
 //
-// A workgroup computes BR x BC outputs in stages of 128 contraction columns
-// (128 bytes of every tile row), which global_load_lds_dwordx4 brings into a
-// ring of LDS buffers.  Tile row r's 16-byte chunk c lies in slot
-// c ^ ((r >> 1) & 7), so a fragment read (16 rows at one chunk per lane
-// quarter) covers all 64 banks.  One barrier per stage; in the 256-wide tiles
-// fragments are read one step of 64 columns ahead of the matrix instructions
-// that take them.  The column operand goes first into the matrix instruction,
-// so a lane holds 4 consecutive columns of one row; results leave through LDS
-// in whole rows.
+// A workgroup computes BR x BC outputs in stages of 128 or 64 contraction
+// columns (as many bytes of every tile row), which global_load_lds_dwordx4
+// brings into a ring of LDS buffers without passing through registers.  Of a
+// row of 128 bytes the 16-byte chunk c lies in slot c ^ ((r >> 1) & 7), of 64
+// bytes in c ^ (-(r >> 2) & 3): a fragment read (ds_read_b128 of 16 rows at one
+// chunk per lane quarter) then meets no bank twice (counter: 0 conflicts; 46%
+// of the LDS cycles with c ^ ((r >> 2) & 3)).  One barrier per stage.  In the
+// tiles that have a CU to themselves fragments are read one step of 64 columns
+// ahead of the matrix instructions that take them; workgroups that share a CU
+// cover each other's waits, and skip the row tiles that a group's last chunk
+// lacks.  The column operand goes first into the matrix instruction, so a lane
+// holds 4 consecutive columns of one row; results leave through LDS in whole
+// rows, after the epilogue.
+//
+// 4096 x 7168 -> 4096: 103 us, 2.33 POP/s (2.33 at 8192^3, where the library's
+// plain product reaches 2.1).  The matrix cores are busy 57% of the cycles at
+// 1.84 GHz: what switches sets the clock (all codes 1: 2.9 POP/s).  Variants with
+// fewer LDS reads (4 waves of 128 x 128 outputs, 2.2 POP/s at 2.07 GHz and 48%
+// busy) or larger matrix instructions (32x32x32: 3.1 POP/s on equal codes, 2.2 on
+// random ones) gain nothing there.  Groups of few rows are bound by their
+// weights: 4096 tokens' down products of 256 experts (3.9 GB read, 0.47 GB
+// written) take 986 us, 4.4 TB/s; 16 rows for each expert 700 us, 5.5 TB/s.
+// Of those, 128 x 256 tiles of 64-column stages, two workgroups per CU, take 3
+// to 10% less than one of three 128-column stages.
 #include <type_traits>
 
 #include "matmul_int8.hpp"
@@ -421,50 +436,58 @@ __global__ __launch_bounds__(256) void m8_join_kernel(M8Args a, int bm) {
 
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// Tile shapes, with the times that the estimate takes (us per stage of 128
-// contraction columns): lat of a workgroup by itself on its CU, thr per
-// workgroup and CU when the chip is full; wgs that share a CU, so that one's
-// start and end hide behind another's stages.  The numbers are fitted to 107
-// products (16 .. 32768 rows, dense and of 2 .. 256 groups, 64 .. 8192 x 64 ..
-// 8192), each timed in every shape and split: the choice is within 6% of the
-// best in 104 of them, the others 13, 15 and 18% off.
+// Tile shapes, with the times that the estimate takes (us): lat per stage of
+// 128 contraction columns and end for its start and writing, of a workgroup by
+// itself on its CU; the same per workgroup and CU when the chip is full, where
+// workgroups that share a CU (`one`: none do) hide each other's ends.  The
+// numbers are fitted to 842 products (10 .. 37000 rows, dense and of 2 .. 256
+// groups, 64 .. 8192 x 64 .. 8192), each timed in every shape and split and, up
+// to 2000 rows, on the few-row kernel: what m8_pick takes is 1.2% off the best
+// in the mean, over 10% off in 5% of them, at most 43%.  Of 320 products that
+// the fit had not seen it is 1.8% off in the mean and over 10% in 25 (at worst
+// 4115 rows of 109 groups 86 -> 269, 16.2 us against 10.1).
 struct M8Shape {
     int br, bc;
-    double lat, thr;
-    int wgs;
+    double lat, end, full_lat, full_end;
+    bool one;
 };
-constexpr M8Shape M8_SHAPES[] = {
-    {256, 256, 1.39, 1.32, 1}, {128, 256, 0.64, 0.93, 1}, {128, 256, 1.16, 1.02, 2}, {128, 128, 0.56, 0.52, 2}, {64, 64, 0.3, 0.17, 3}};
+constexpr M8Shape M8_SHAPES[] = {{256, 256, 0.926, 1.34, 1.58, 8.0, true},
+                                 {128, 256, 0.738, 1.41, 0.842, 6.31, true},
+                                 {128, 256, 0.937, 2.82, 1.108, 1.92, false},
+                                 {128, 128, 0.434, 2.73, 0.54, 0.85, false},
+                                 {64, 64, 0.363, 2.65, 0.143, 0.93, false}};
 constexpr int M8_NSHAPES = 5;
-constexpr double M8_ENDS = 2.35;   // us to fill a workgroup's first stages and to write its tile
-constexpr double M8_JOIN = 3.0;    // us of a join launch
-// Rounds of workgroups up to which each scans for its chunk: 256 rows of 8 groups
+constexpr double M8_JOIN = 1.5;     // us of a join launch
+constexpr double M8_MEM = 2.1e6;    // bytes per us of partial sums
+constexpr double M8_READ = 18.5e6;  // bytes per us of both operands into LDS, of groups whose weights
+constexpr double M8_FAR = 13.6e6;   // the 256 MB of the memory-side cache hold, or not
+// Workgroups per CU up to which each scans for its chunk: 256 rows of 8 groups
 // 2048 -> 2048 13.2 us against 14.9 with a plan launch, 4096 of 8 41.8 / 42.3,
 // but 32768 of 64 256 -> 4096 290 / 249, 16000 of 1000 512 -> 512 78 / 63.
-constexpr double M8_SCANS = 2.0;
-constexpr double M8_MEM = 4.2e6;   // bytes per us, of outputs and partial sums
+constexpr double M8_SCANS = 4.0;
 
-// Tile shape and contraction splits of the least estimated time: a CU's
-// workgroups times their stages, plus what does not overlap.
+// Tile shape and contraction splits of the least estimated time.
 M8Pick m8_tile_pick(int P, int K, int N, int E) {
     const int live = E < P ? E : P;
-    const int ns = cdiv(K, M8_K);
+    const int all = cdiv(K, M8_K);
     M8Pick best{0, 1, 1e300};
     for (int i = 0; i < M8_NSHAPES; ++i) {
         const M8Shape& t = M8_SHAPES[i];
         double tr = cdiv(P, t.br);   // row tiles; of ragged groups about half a tile each is not filled
         if (E > 1) tr = (double)P / t.br + 0.5 * live > live ? (double)P / t.br + 0.5 * live : live;
         const double tiles = tr * cdiv(N, t.bc);
-        const double out = tiles * t.br * t.bc * 2.0 / M8_MEM;
-        for (int s = 1; s <= M8_MAX_SPLITS && (s == 1 || (i >= 3 && ns / s >= 4 && tiles * s <= 512.0)); s *= 2) {
-            const double wgs = tiles * s, per_cu = wgs <= 256.0 ? wgs / 256.0 : (double)(int64_t)(wgs / 256.0 + 0.999);
-            const double stage = t.thr * per_cu > t.lat ? t.thr * per_cu : t.lat;
-            double us = stage * cdiv(ns, s);
-            if (t.wgs == 1)
-                us += M8_ENDS * (per_cu < 1.0 ? 1.0 : per_cu) + out;
-            else
-                us = (us > out ? us : out) + M8_ENDS;
-            if (s > 1) us += M8_JOIN + (double)wgs * t.br * t.bc * 8.0 / M8_MEM;
+        for (int s = 1; s <= M8_MAX_SPLITS && (s == 1 || (i >= 3 && all / s >= 4 && tiles * s <= 512.0)); s *= 2) {
+            const int stages = cdiv(all, s);
+            double per_cu = tiles * s / 256.0;
+            if (t.one) per_cu = (double)(int64_t)(per_cu + 0.999);
+            const double alone = t.lat * stages + t.end, full = per_cu * (t.full_lat * stages + t.full_end);
+            double us = alone > full ? alone : full;
+            if (E > 1) {
+                const double read = tiles * (t.br + t.bc) * K /
+                                    ((double)live * N * K < (double)(1 << 28) ? M8_READ : M8_FAR);
+                us = us > read ? us : read;
+            }
+            if (s > 1) us += M8_JOIN + tiles * s * t.br * t.bc * 8.0 / M8_MEM;
             if (us < best.us) best = M8Pick{i, s, us};
         }
     }
@@ -507,7 +530,7 @@ int m8_chunk_rows(const M8Pick& pick) { return pick.shape < 0 ? 0 : M8_SHAPES[pi
 bool m8_wants_plan(const M8Pick& pick, int P, int N, int E) {
     const M8Shape& t = M8_SHAPES[pick.shape];
     const double tiles = ((double)P / t.br + 0.5 * (E < P ? E : P)) * cdiv(N, t.bc);
-    return pick.splits > 1 || tiles > M8_SCANS * 256.0 * t.wgs;
+    return pick.splits > 1 || tiles > M8_SCANS * 256.0;
 }
 
 size_t m8_split_bytes(const M8Pick& pick, int P, int N) {

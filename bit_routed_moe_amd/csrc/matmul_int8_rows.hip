@@ -2,14 +2,17 @@
 // into registers, and the time is that of reading them.
 //
 // A workgroup takes one chunk of at most 16 rows of a group and 16 * RT weight
-// rows (SwiGLU: 16 gate rows and the 16 up rows they pair with); its 8 waves share the
-// contraction KW ways (and weight rows 8 / KW ways where the contraction is
-// short).  A step is 128 contraction columns, 2 loads of 64 contiguous bytes
+// rows (SwiGLU: 16 gate rows and the 16 up rows they pair with); its 8 waves
+// share the contraction KW ways (and weight rows 8 / KW ways where the
+// contraction is short).  A step is 128 contraction columns, 2 loads of 64 contiguous bytes
 // of each of 16 weight rows, four steps in flight per wave (steps of 256
 // columns, two in flight: 12.1 against 11.3 us at one row of 7168 -> 7168, 4.2
 // against 3.6 at 1024 -> 1024).
 // Weights go first into the matrix instruction (v_mfma_i32_16x16x64_i8), so a
-// lane's results belong to one row.  The waves' sums are joined in LDS.
+// lane's results belong to one row.  The waves' sums are joined in LDS.  One row
+// of 7168 -> 7168: 11.3 us (weights at 4.5 TB/s, launch included); one token's
+// gate/up products of 8 experts 7168 -> 4096 41.7 us (5.6 TB/s); 16 rows of
+// 7168 -> 40000 59 us.
 //
 // The rows' group is found from the offsets in the kernel (a plan launch would
 // cost more than the product), by a scan over the groups' numbers of chunks, or
@@ -231,18 +234,18 @@ hipError_t w8_run(const M8Args& a, hipStream_t s) {
 
 }  // namespace
 
-// Products that take these kernels.  Up to 8 rows (16 below 32768 columns;
-// grouped 16, or 256 at two per group) the weights come from memory once in
-// either kernel, and these read them faster: 9 rows of 7168 -> 7168 13.3 us
-// against 16.0 on the tiles, 16 of 7168 -> 131072 176 / 162, 64 of 256 groups
-// 7168 -> 4096 269 / 300, 256 of 256 807 / 817; at worst 12 rows of 4096 ->
-// 16384 17.0 / 16.0.  More rows read small weights again from L2 for each 16,
-// which the tiles' latency outlasts for a while (301 x 1459 -> 331 4.8 / 8.3,
-// 1200 10.4 / 8.5; 903 rows of 7 groups 459 -> 331 7.0 / 9.3): there an estimate
-// decides, of the time for all workgroups, for a wave's steps and for the bytes
-// read.  Of 175 products timed both ways it is over 8% off in 3, at most 16%.
+// Products that take these kernels.  Up to 8 rows (16 below 32768 columns, and
+// of groups) the weights come from memory once in either kernel, and these read
+// them faster: 9 rows of 7168 -> 7168 13.3 us against 16.0 on the tiles, 16 of
+// 7168 -> 131072 176 / 162; at worst 12 rows of 4096 -> 16384 17.0 / 16.0.  More
+// rows read small weights again from L2 for each 16, which the tiles' latency
+// outlasts for a while (301 x 1459 -> 331 4.8 / 8.3, 1200 10.4 / 8.5; 903 rows
+// of 7 groups 459 -> 331 7.0 / 9.3), and few rows of many groups read them once
+// here too (64 of 256 groups 7168 -> 4096 269 / 300, 256 of 256 807 / 817):
+// there an estimate decides, of the time for all workgroups, for a wave's steps
+// and for the bytes read, fitted together with the tiles'.
 bool m8_rows_takes(int P, int K, int N, int E, double tile_us) {
-    if (E > 1 ? P <= 16 || (P <= 256 && P <= 2 * E) : P <= 8 || (P <= 16 && N < 32768)) return true;
+    if (E > 1 ? P <= 16 : P <= 8 || (P <= 16 && N < 32768)) return true;
     if (P > 1 << 19) return false;   // (chunks are a dimension of the grid, at most 65535)
     const int kw = w8_kw(K), ng = W8_WAVES / kw;
     const double chunks = E == 1 ? (P + 15) / 16 : P / 16.0 + (E < P ? E : P) / 2.0;
@@ -251,8 +254,8 @@ bool m8_rows_takes(int P, int K, int N, int E, double tile_us) {
     const double wgs = chunks * ((N + per - 1) / per) / 256.0;   // per CU
     const int steps = ((K / W8_STEP + kw - 1) / kw + (K % W8_STEP != 0)) * (two ? 2 : 1);
     const double mb = chunks * N * K / (1 << 20);
-    if (E == 1) return 3.53 + 1.12 * wgs + 0.226 * steps + 0.06 * mb < tile_us + 2.75;
-    return 4.3 + 1.51 * wgs + 0.024 * steps + 0.161 * mb < tile_us + 4.25;   // (a plan, or scans, on top)
+    if (E == 1) return 1.75 + 0.565 * wgs + 0.274 * steps + 0.12 * mb < tile_us;
+    return 2.15 + 0.795 * wgs + 0.032 * steps + 0.204 * mb < tile_us + 3.0;   // (a plan, or scans, on top)
 }
 
 hipError_t launch_m8_rows(const M8Args& a, bool f32, hipStream_t s) {
