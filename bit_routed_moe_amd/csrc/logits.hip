@@ -7,15 +7,16 @@
 //   l = -infinity unless v's bit is set in the row's mask
 //
 // Bound by memory: each logit is read and written once.  A workgroup takes one
-// segment of a row.  It requests its logits first (those in 16-byte pieces that
-// the mask leaves something of), then reads the row's whole history and biases
-// and notes those of its segment in LDS (a count per token, the generated ones
-// added and the prompt's in the top bit; the place of its last bias): integer
-// atomics, whose order changes nothing.  64 rows of 131072 fp32 under all rules
+// segment of a row.  It requests the row's lists and its logits (those in
+// 16-byte pieces that the mask leaves something of) before it waits for any,
+// then notes the history's and the biases' tokens of its segment in LDS (a count
+// per token, the generated ones added and the prompt's in the top bit; the place
+// of its last bias): integer atomics, whose order changes nothing.  64 rows of 131072 fp32 under all rules
 // (histories of 2000 tokens, half of the rows masked; 68 MB) 14.6 us, 4.6 TB/s;
 // 256 rows of 50003 bf16 to fp32 with counts (77 MB) 16.9 us, 4.6 TB/s; one row
-// of 131072 5.6 us, the latency of its lists and of LDS.  Lists first requested
-// behind the logits: 23.7, 19.4 and 8.4 us.
+// of 131072 5.6 us, the latency of its lists and of LDS.  With the lists
+// requested behind the logits, both tables always and 4096-token segments of
+// 256 threads: 23.7, 19.4 and 8.4 us.
 #include "common.hpp"
 #include "launch.hpp"
 
