@@ -505,3 +505,47 @@ def test_experts_in_8_bits_to_the_next_token():
     assert ((lg.double() - want).abs()[allowed] <= 4 * EPS * want.abs()[allowed]).all()
     assert (lg[~allowed] == float("-inf")).all()
     assert torch.equal(token.long(), torch.where(allowed, lg, float("-inf")).argmax(1))
+
+
+# rows, K, N, groups (None: dense): the wide tiles of 128 rows with and without their pipeline, and contractions
+# in 2, 4, 8 and 16 parts, whose ends leave a part with fewer steps, or rows of a tile without a row
+PARTS = [(32679, 2707, 230, None), (69, 11360, 9010, None), (4165, 10355, 82, None), (2055, 16263, 126, None),
+         (59, 15945, 286, None), (53, 2762, 4826, None), (3485, 3391, 62, None), (19, 15416, 2122, None),
+         (736, 2157, 494, [2] * 128 + [0] * 64 + [1] * 32 + [14] * 32),
+         (24, 3806, 10590, [0, 17, 1, 1, 0, 3, 1, 1]), (120, 5625, 1402, [100, 0, 3, 1, 0, 16, 0, 0]),
+         (616, 12114, 118, [0, 129, 64, 1, 0, 300, 65, 57]), (1351, 15895, 54, [1000, 0, 55, 296]),
+         (2195, 6312, 62, [34] * 64 + [0]), (4446, 10690, 66, [4000, 1, 0, 128, 129, 60, 64, 64]),
+         (2733, 1197, 5814, None)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,K,N,groups", PARTS, ids=lambda v: str(v)[:12])
+def test_wide_tiles_and_parts(rows, K, N, groups, dtype):
+    for act, k in (("none", 0), ("swiglu", 3)):
+        rows_ = rows if groups is None else sum(groups)
+        p = Problem(rows_ + (5 if groups else 0), K, N, dtype, act=act, groups=groups, gather_k=k if groups else 0,
+                    bias=True, residual=groups is None, gap=1, seed=k)
+        first = p.run()[:rows_].clone()
+        p.check()
+        assert torch.equal(p.run()[:rows_], first)
+
+
+@pytest.mark.parametrize("rows,K,N,groups", [(69, 11360, 9010, None), (59, 15945, 286, None), (53, 2762, 4826, None),
+                                             (120, 5625, 1402, [100, 0, 3, 1, 0, 16, 0, 0])], ids=lambda v: str(v)[:12])
+def test_parts_in_a_graph(rows, K, N, groups):
+    """The sums of the parts are written anew on every replay, whatever the workspace holds by then."""
+    p = Problem(rows, K, N, "bf16", act="silu", groups=groups, bias=True)
+    want = p.run().clone()
+    p.check()
+    ws, y = p.workspace(), torch.empty_like(p.yb)[:, :p.oc]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.run(y=y, ws=ws)
+    for _ in range(3):
+        y.zero_()
+        ws.fill_(0x5A)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        assert torch.equal(p.run(), want)
