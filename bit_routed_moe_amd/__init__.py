@@ -476,6 +476,8 @@ def _own_rows(name, t, dtype, rows, cols, q, dev):
     multiple of q.)"""
     shape, strides = t.shape, t.stride()
     ld = -(-cols // q) * q if rows == 1 else strides[-2] if len(shape) > 1 and shape[-2] > 1 else cols
+    if ld < cols:                            # (rows on one another; the library takes 0 for rows without gaps)
+        raise Ds4MoeError(-2, f"{name} of shape {tuple(shape)}, strides {strides}: rows of {cols} elements, {ld} apart")
     # (two dimensions first, as in _matrix)
     if len(shape) == 2 and shape[0] >= rows and shape[1] >= cols and strides[1] == 1 and t.dtype is dtype:
         if t.get_device() != dev:

@@ -1,0 +1,46 @@
+"""Tensors whose memory is not what their shape says: the bindings of the rows'
+quantization and of the rules on logits refuse them (no GPU: nothing here
+reaches one)."""
+import pytest
+import torch
+
+ds4 = pytest.importorskip("bit_routed_moe_amd")
+
+I8 = torch.int8
+
+
+class Recorder:
+    def __init__(self):
+        self.called = []
+
+    def __getattr__(self, name):
+        return lambda *args: self.called.append((name, args)) or 0
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(ds4, "lib", r)
+    monkeypatch.setattr(ds4, "_here", lambda: -1)
+    monkeypatch.setattr(ds4, "_s", lambda *args: None)
+    return r
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_quantize_refuses_rows_closer_than_their_columns(lib, dtype):
+    """A stride of 0 (one row, broadcast) is no "without gaps", and rows may not overlap."""
+    rows, cols = 5, 64
+    good = dict(x=torch.zeros(rows, cols, dtype=dtype), codes=torch.zeros(rows, cols, dtype=I8), scale=torch.zeros(rows))
+    ds4.quantize_rows_int8(rows, cols, **good)
+    assert lib.called.pop()[0] == "ds4moe_quantize_rows_int8"
+    for name in ("x", "codes"):
+        t = good[name]
+        for bad in (t[:1].expand(rows, cols), t[:1, None].expand(rows, 1, cols), t[None, :1].expand(1, rows, cols),
+                    t.as_strided((rows, cols), (16, 1)), t[0].expand(2, 3, cols)):
+            with pytest.raises(ds4.Ds4MoeError, match=name) as e:
+                ds4.quantize_rows_int8(rows, cols, **dict(good, **{name: bad}))
+            assert e.value.status == -2 and not lib.called, (name, bad.shape, bad.stride())
+    # one row has no stride: any is taken
+    ds4.quantize_rows_int8(1, cols, good["x"][:1].expand(rows, cols), good["codes"][:1].expand(rows, cols), good["scale"])
+    a = lib.called.pop()[1]
+    assert a[4] >= cols and a[6] >= cols
