@@ -650,6 +650,8 @@ def adjust_logits(B, V, logits, out, history=None, history_offsets=None, prompt_
             raise Ds4MoeError(-2, f"mask of shape {tuple(mask.shape)}, strides {mask.stride()} for {V} tokens")
         if mask.get_device() != dev:
             raise Ds4MoeError(-1, f"mask on {mask.device}, not on the current HIP device {dev}")
+        if mask.shape[0] == 0 and mask_row is None:   # (without memory: the library would take it for no mask)
+            raise Ds4MoeError(-2, f"0 mask rows for {B} rows without mask_row")
         r.mask, r.mask_rows = mask.data_ptr(), mask.shape[0]
         r.mask_ld = mask.stride(0) if mask.shape[0] > 1 else words
     _check(lib.ds4moe_adjust_logits(B, V, src, ld, dt, ctypes.byref(r), dst, ldo, odt, _s(stream, dev)))

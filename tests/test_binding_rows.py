@@ -44,3 +44,19 @@ def test_quantize_refuses_rows_closer_than_their_columns(lib, dtype):
     ds4.quantize_rows_int8(1, cols, good["x"][:1].expand(rows, cols), good["codes"][:1].expand(rows, cols), good["scale"])
     a = lib.called.pop()[1]
     assert a[4] >= cols and a[6] >= cols
+
+
+def test_mask_without_rows_is_no_mask_left_out(lib):
+    """An empty tensor has no memory; without mask_row its rows are too few, which is not the rule switched off."""
+    B, V = 3, 100
+    call = lambda **kw: ds4.adjust_logits(B, V, torch.zeros(B, V), torch.zeros(B, V), **kw)
+    for words in (4, 9):
+        empty = torch.zeros(0, words, dtype=torch.int32)
+        with pytest.raises(ds4.Ds4MoeError, match="mask") as e:
+            call(mask=empty)
+        assert e.value.status == -2 and not lib.called
+        call(mask=empty, mask_row=torch.zeros(B, dtype=torch.int32))     # (every row's mask_row is then outside: no mask)
+        assert lib.called.pop()[0] == "ds4moe_adjust_logits"
+    call(mask=torch.zeros(B, 4, dtype=torch.int32))
+    r = lib.called.pop()[1][5]._obj
+    assert r.mask and r.mask_rows == B
