@@ -57,6 +57,19 @@ __device__ __forceinline__ void m8_st8(T* p, const float (&v)[8], int n, bool ve
     }
 }
 
+// sum * xs * ws.  sum is below 2^31, so sum * xs stays in fp32 for |xs| < 2^96;
+// from there on 2^-64 of it is taken first and given back last, both exact, so
+// that nothing on the way to a z that fp32 holds is infinite.  (Small scales lose
+// nothing: sum is a whole number.)
+struct M8RowScale {
+    float s;
+    bool far;
+};
+__device__ __forceinline__ M8RowScale m8_row_scale(float xs) {
+    const bool far = fabsf(xs) >= 0x1p96f;
+    return {far ? xs * 0x1p-64f : xs, far};
+}
+
 // z of 8 columns from n on (cnt of them exist) of a row with scale xs.
 template <typename T>
 __device__ __forceinline__ void m8_z8(const M8Args& a, int e, float xs, int n, int cnt, const int32_t (&sum)[8],
@@ -64,8 +77,13 @@ __device__ __forceinline__ void m8_z8(const M8Args& a, int e, float xs, int n, i
     const size_t o = (size_t)e * a.N + n;      // (rows of an odd N start anywhere)
     float ws[8];
     m8_ld8(a.ws + o, cnt, cnt >= 8 && (o & 3) == 0, ws);
+    const M8RowScale rs = m8_row_scale(xs);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = (float)sum[i] * xs * ws[i];
+    for (int i = 0; i < 8; ++i) z[i] = (float)sum[i] * rs.s * ws[i];
+    if (__builtin_expect(rs.far, 0)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] *= 0x1p64f;
+    }
     if (a.bias) {
         float b[8];
         m8_ld8(static_cast<const T*>(a.bias) + o, cnt, cnt >= 8 && (o & (16 / sizeof(T) - 1)) == 0, b);

@@ -170,7 +170,7 @@ __global__ __launch_bounds__(64 * W8_WAVES) void w8_kernel(M8Args a, int kw, int
         const int c = (blockIdx.x * ng + g) * per + rr;
         if (c >= cols) continue;
         const int r = row0 + tok;
-        const float xs = a.xs[mm_src(a, r)];
+        const M8RowScale rs = m8_row_scale(a.xs[mm_src(a, r)]);
         float z[GLU ? 2 : 1];
 #pragma unroll
         for (int t = 0; t < (GLU ? 2 : 1); ++t) {
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(64 * W8_WAVES) void w8_kernel(M8Args a, int kw, int
             int32_t sum = 0;
             for (int k = 0; k < kw; ++k) sum += p[(size_t)k * RT * 64 * 4];
             const size_t o = (size_t)group * a.N + c + (t ? cols : 0);
-            z[t] = (float)sum * xs * a.ws[o];
+            z[t] = (float)sum * rs.s * a.ws[o] * (rs.far ? 0x1p64f : 1.0f);
             if (a.bias) z[t] += mm_ld(static_cast<const T*>(a.bias) + o);
         }
         float v;
