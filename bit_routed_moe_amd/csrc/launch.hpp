@@ -225,7 +225,12 @@ struct LogitArgs {
 };
 hipError_t launch_adjust_logits(const LogitArgs& a, bool f32_in, bool f32_out, hipStream_t s);
 
-// Rows to 8-bit integers with a scale each (quant_rows.hip).
+// Rows to 8-bit integers with a scale each (quant_rows.hip): waves per row, and
+// a launch's threads and workgroups along x and y.
+struct QuantGrid {
+    int waves, threads, x, y;
+};
+QuantGrid quantize_rows_grid(int rows, int K, bool f32);
 hipError_t launch_quantize_rows(int rows, int K, bool f32, const void* x, int64_t ldx, int8_t* codes, int64_t ldq,
                                 float* scale, hipStream_t s);
 

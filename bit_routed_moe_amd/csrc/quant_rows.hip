@@ -131,7 +131,7 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void qr_kernel(int rows, int 
                                                                  float* __restrict__ scale) {
     constexpr int HELD = 4, NT = 64 * W, RPB = W > 4 ? 1 : 4 / W;
     const int tid = threadIdx.x % NT, sub = threadIdx.x / NT;
-    const int64_t row = (int64_t)blockIdx.x * RPB + sub;
+    const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * RPB + sub;
     const bool has = row < rows;
     const T* const xr = x + (size_t)(has ? row : 0) * ldx;
     const int chunks = (K + QrVec<T>::N - 1) / QrVec<T>::N;
@@ -168,17 +168,28 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void qr_kernel(int rows, int 
 
 template <typename T>
 hipError_t qr_run(int rows, int K, const T* x, int64_t ldx, int8_t* codes, int64_t ldq, float* scale, hipStream_t s) {
-    const int chunks = (K + QrVec<T>::N - 1) / QrVec<T>::N;
-    if (chunks <= 4 * 64)   // a wave holds the row
-        qr_kernel<T, 1><<<(uint32_t)((rows + 3) / 4), 256, 0, s>>>(rows, K, x, ldx, codes, ldq, scale);
-    else if (rows <= 256)   // fewer rows than CUs: 16 waves each
-        qr_kernel<T, 16><<<(uint32_t)rows, 1024, 0, s>>>(rows, K, x, ldx, codes, ldq, scale);
+    const QuantGrid q = quantize_rows_grid(rows, K, sizeof(T) == 4);
+    const dim3 g((uint32_t)q.x, (uint32_t)q.y);
+    if (q.waves == 1)
+        qr_kernel<T, 1><<<g, q.threads, 0, s>>>(rows, K, x, ldx, codes, ldq, scale);
+    else if (q.waves == 16)
+        qr_kernel<T, 16><<<g, q.threads, 0, s>>>(rows, K, x, ldx, codes, ldq, scale);
     else
-        qr_kernel<T, 4><<<(uint32_t)rows, 256, 0, s>>>(rows, K, x, ldx, codes, ldq, scale);
+        qr_kernel<T, 4><<<g, q.threads, 0, s>>>(rows, K, x, ldx, codes, ldq, scale);
     return hipGetLastError();
 }
 
 }  // namespace
+
+QuantGrid quantize_rows_grid(int rows, int K, bool f32) {
+    const int per = f32 ? QrVec<float>::N : QrVec<uint16_t>::N, pieces = (K + per - 1) / per;
+    // a wave where it holds the row, 16 where there are fewer rows than CUs, else 4
+    const int waves = pieces <= 4 * 64 ? 1 : (rows <= 256 ? 16 : 4);
+    const int threads = waves == 16 ? 1024 : 256, at_once = threads / (64 * waves);
+    // (a launch's threads along one dimension have to be below 2^32)
+    const int blocks = (rows + at_once - 1) / at_once, y = blocks > (1 << 23) ? 2 : 1;
+    return QuantGrid{waves, threads, (blocks + y - 1) / y, y};
+}
 
 hipError_t launch_quantize_rows(int rows, int K, bool f32, const void* x, int64_t ldx, int8_t* codes, int64_t ldq,
                                 float* scale, hipStream_t s) {
