@@ -156,6 +156,7 @@ def _types():
 
 
 _F32, _BF16, _I32, _I8 = _types()
+_I32_MAX = (1 << 31) - 1
 
 
 def _lookups():
@@ -633,6 +634,8 @@ def adjust_logits(B, V, logits, out, history=None, history_offsets=None, prompt_
     odt, ldo, dst = _logit_rows("out", out, B, V, dev)
     nh = 0 if history is None else history.numel()
     nb = 0 if bias_token is None else bias_token.numel()
+    if nh > _I32_MAX or nb > _I32_MAX:
+        raise Ds4MoeError(-2, f"history of {nh} tokens, bias_token of {nb}: more than their offsets reach")
     # (an empty list is a list all the same; it need not have memory)
     r = LogitRules(
         _vector("history", history, _I32, nh, dev), _vector("history_offsets", history_offsets, _I32, B + 1, dev),

@@ -60,3 +60,20 @@ def test_mask_without_rows_is_no_mask_left_out(lib):
     call(mask=torch.zeros(B, 4, dtype=torch.int32))
     r = lib.called.pop()[1][5]._obj
     assert r.mask and r.mask_rows == B
+
+
+def test_lists_beyond_their_offsets_reach_are_refused(lib):
+    """Offsets are int32: a longer list's length would be passed modulo 2^32, and its rules be left out.  (Tensors
+    without memory stand for the 16 GB.)"""
+    B, V = 3, 100
+    i = lambda *s, **kw: torch.zeros(*s, dtype=torch.int32, **kw)
+    good = dict(history=i(9), history_offsets=i(B + 1), bias_token=i(4), bias_value=torch.zeros(4), bias_offsets=i(B + 1))
+    call = lambda **kw: ds4.adjust_logits(B, V, torch.zeros(B, V), torch.zeros(B, V), **dict(good, **kw))
+    call()
+    lib.called.pop()
+    for n in (1 << 31, (1 << 32) + 5):
+        for kw in (dict(history=i(n, device="meta")),
+                   dict(bias_token=i(n, device="meta"), bias_value=torch.zeros(n, device="meta"))):
+            with pytest.raises(ds4.Ds4MoeError, match="history|bias_token") as e:
+                call(**kw)
+            assert e.value.status == -2 and not lib.called
