@@ -14,14 +14,15 @@
 // holds 4 consecutive columns of one row; results leave through LDS in whole
 // rows, after the epilogue.
 //
-// 4096 x 7168 -> 4096: 103 us, 2.33 POP/s (2.33 at 8192^3, where the library's
-// plain product reaches 2.1).  The matrix cores are busy 57% of the cycles at
-// 1.84 GHz: what switches sets the clock (all codes 1: 2.9 POP/s).  Variants with
-// fewer LDS reads (4 waves of 128 x 128 outputs, 2.2 POP/s at 2.07 GHz and 48%
-// busy) or larger matrix instructions (32x32x32: 3.1 POP/s on equal codes, 2.2 on
-// random ones) gain nothing there.  Groups of few rows are bound by their
-// weights: 4096 tokens' down products of 256 experts (3.9 GB read, 0.47 GB
-// written) take 986 us, 4.4 TB/s; 16 rows for each expert 700 us, 5.5 TB/s.
+// 4096 x 7168 -> 4096: 104 to 108 us by run, 2.2 to 2.3 POP/s (2.4 at 8192^3,
+// where the library's plain product reaches 2.1).  The matrix cores are busy 57%
+// of the cycles at 1.84 GHz: what switches sets the clock (all codes 1: 2.9
+// POP/s).  Variants with fewer LDS reads (4 waves of 128 x 128 outputs, 2.2 POP/s
+// at 2.07 GHz and 48% busy) or larger matrix instructions (32x32x32: 3.1 POP/s on
+// equal codes, 2.2 on random ones) gain nothing there.  Groups of few rows are
+// bound by their weights: 4096 tokens' down products of 256 experts (3.9 GB read,
+// 0.47 GB written) take 986 to 1026 us, 4.3 TB/s; 16 rows for each expert 700 us,
+// 5.5 TB/s.
 // Of those, 128 x 256 tiles of 64-column stages, two workgroups per CU, take 3
 // to 10% less than one of three 128-column stages.
 #include <type_traits>

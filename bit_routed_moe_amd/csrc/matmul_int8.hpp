@@ -57,10 +57,10 @@ __device__ __forceinline__ void m8_st8(T* p, const float (&v)[8], int n, bool ve
     }
 }
 
-// sum * xs * ws.  sum is below 2^31, so sum * xs stays in fp32 for |xs| < 2^96;
-// from there on 2^-64 of it is taken first and given back last, both exact, so
-// that nothing on the way to a z that fp32 holds is infinite.  (Small scales lose
-// nothing: sum is a whole number.)
+// A row's scale as sum * xs * ws takes it.  A sum is at most 2^31, so sum * xs
+// stays in fp32 for |xs| < 2^96; from there on 2^-64 of the scale comes first and
+// 2^64 last, both exact, so that nothing on the way to a z that fp32 holds is
+// infinite.  (Small scales lose nothing: sum is a whole number.)
 struct M8RowScale {
     float s;
     bool far;
